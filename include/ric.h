@@ -476,6 +476,163 @@ int ric_check_slots(const int32_t* slot_mapping, int32_t num_tokens, const int32
 int ric_check_slots_noalloc(const int32_t* slot_mapping, int32_t num_tokens, const int32_t* dev_num_tokens,
                             int64_t num_slots, int32_t* dev_result, void* stream);
 
+/* ---- attention over the paged cache ----------------------------------------- */
+
+#define RIC_F16  0
+#define RIC_BF16 1
+#define RIC_F32  2
+
+/* What an attention layer is, independent of the step. */
+typedef struct {
+    int32_t dtype;                /* RIC_F16 or RIC_BF16: q, caches and out                       */
+    int32_t num_heads;            /* query heads, a multiple of num_kv_heads: query head h reads
+                                     K/V head h / (num_heads / num_kv_heads)                      */
+    int32_t num_kv_heads;
+    int32_t head_dim;             /* multiple of 8, 8..256                                        */
+    int32_t block_size;           /* tokens per cache page                                        */
+    float scale;                  /* scores are scale * q.k                                       */
+    float softcap;                /* c > 0: scores become c * tanh(score / c); 0: no cap          */
+    int32_t window;               /* w > 0: position p sees only keys j > p - w; 0: no window     */
+    const float* alibi_slopes;    /* DEVICE float[num_heads]: slope * |p - j| is subtracted from
+                                     the (capped) score; NULL: no bias                            */
+    const int32_t* prefix_lens;   /* DEVICE int32[num_reqs]: request i's keys j < prefix_lens[i]
+                                     are visible to all its queries, later ones included (inside
+                                     the window); NULL: causal only                               */
+} ric_attention;
+
+/* Attention of the step's new tokens over their requests' pages: chunks,
+ * single tokens and both in one call ([P1 §3. 物理 KV 槽位], [P3 §实现]: the
+ * K/V rows written through slot_mapping are read back through the block table).
+ * Query token t of request i (query_start_loc[i] <= t < query_start_loc[i+1],
+ * n_i tokens) stands at position p = seq_lens[i] - n_i + t - query_start_loc[i].
+ * Key j < seq_lens[i] lies in row j % block_size of page block_table[i][j /
+ * block_size] and is visible if (j <= p or j < prefix_lens[i]) and (window == 0
+ * or j > p - window).  With s_j the score above,
+ *     out[t][h] = sum_j exp(s_j - max) v_j / sum_j exp(s_j - max)
+ * over the visible keys; a row whose visible keys leave no score above -inf
+ * (none visible, p < 0 included) gets zeros.  Sums and statistics are held in
+ * 32 bits.  Keys that a row does not see never reach it, whatever their pages
+ * hold (NaN and infinities included).
+ *   q, out       DEVICE [num_tokens][num_heads][head_dim]; token strides in bytes
+ *                (0: num_heads * head_dim * 2), multiples of 16.  out may be q
+ *                itself (same address and stride), but not overlap it otherwise
+ *   k_cache, v_cache  DEVICE [num_blocks][block_size][num_kv_heads][head_dim],
+ *                contiguous (the layout ric_reshape_and_cache writes)
+ *   block_table  DEVICE int32: row i at block_table + i * block_table_stride, its
+ *                first block_table_width entries readable.  A key whose page id
+ *                lies outside [0, num_blocks), or past the table's width, is left
+ *                out of its row; *dev_status (optional) is then raised.  Ids of
+ *                invisible keys are not looked at
+ *   query_start_loc, seq_lens  DEVICE int32[num_reqs + 1], [num_reqs]
+ *                (ric_step's arrays).  Rows of out outside every request
+ *                (t >= query_start_loc[num_reqs], padding) are left untouched
+ *   max_query_len  no request may have more query tokens: one that has keeps its
+ *                rows of out as they were and raises *dev_status
+ *   max_seq_len  longest request expected; only the way the work is split goes
+ *                by it (a longer one is still right)
+ *   workspace    DEVICE, ric_paged_attention_workspace_bytes() of the same
+ *                arguments (may be 0: then NULL), 16-byte aligned, contents
+ *                undefined after the call.  Calls that may run at the same time
+ *                (two streams, two graphs) need one each
+ * Everything is read on the device, so a captured call replays with new counts
+ * as long as num_reqs, num_tokens and max_query_len still bound them.  Runs on the
+ * current device.  num_tokens <= 2^22.  Equal inputs give equal bits.  Errors:
+ * EINVAL (shapes, strides, alignment, NULL, workspace too small), EHIP. */
+size_t ric_paged_attention_workspace_bytes(const ric_attention* a, int32_t num_reqs, int32_t num_tokens,
+                                           int32_t max_query_len, int32_t max_seq_len);  /* 0 also on EINVAL */
+int ric_paged_attention(const ric_attention* a, const void* q, int64_t q_stride, const void* k_cache,
+                        const void* v_cache, int64_t num_blocks, const int32_t* block_table,
+                        int64_t block_table_stride, int32_t block_table_width, const int32_t* query_start_loc,
+                        const int32_t* seq_lens, int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
+                        int32_t max_seq_len, void* out, int64_t out_stride, void* workspace,
+                        size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ---- log probabilities ------------------------------------------------------- */
+
+/* For each row r < count (count = min(max_rows, *dev_count) or max_rows when
+ * dev_count is NULL, as in ric_gather_rows) of logits x[r][0..vocab), with
+ * m = max x, S = sum exp(x - m):
+ *   logprob[r]  = x[target] - m - ln S          for target = targets[r]
+ *   rank[r]     = 1 + tokens ordered before the target: a higher logit, or an
+ *                 equal one with a lower id
+ *   entropy[r]  = -sum p ln p (a token of probability 0 adds nothing)
+ *   top_ids[r][k], top_logprobs[r][k]  the first top_k tokens of that order
+ * A target outside [0, vocab) has no token: logprob 0, rank 0; one >= vocab also
+ * raises *dev_status (optional).  A logit of -inf is a token of probability 0
+ * (logprob -inf); a row of nothing else has logprobs of -inf and entropy 0.  A
+ * row with a NaN or a +inf has NaN logprobs and entropy; NaN is ordered first.
+ * Rows >= count of the outputs are left untouched.  Sums are held in 32 bits.
+ *   logits       DEVICE, dtype RIC_F16 / RIC_BF16 / RIC_F32, row r at logits +
+ *                r * row_stride bytes (0: vocab elements; a multiple of the
+ *                element size, >= the row; the rows' own alignment is free)
+ *   targets      DEVICE int32[max_rows], or NULL: no target (then logprob and
+ *                rank must be NULL)
+ *   top_k        0..RIC_MAX_TOP_LOGPROBS and <= vocab; 0: top_ids, top_logprobs NULL
+ *   logprob, rank, entropy  DEVICE float / int32 / float [max_rows]; entropy may
+ *                be NULL
+ *   top_ids, top_logprobs  DEVICE int32 / float [max_rows][top_k]
+ *   workspace    DEVICE, ric_token_logprobs_workspace_bytes() bytes (may be 0),
+ *                16-byte aligned; one per call that may run at the same time
+ * Runs on the current device.  max_rows <= 2^22.  Equal inputs give equal bits.
+ * Errors: EINVAL, EHIP. */
+#define RIC_MAX_TOP_LOGPROBS 64
+size_t ric_token_logprobs_workspace_bytes(int32_t max_rows, int32_t vocab, int32_t top_k);
+int ric_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* targets,
+                       const int32_t* dev_count, int32_t max_rows, int32_t vocab, int32_t top_k, float* logprob,
+                       int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ---- pages ------------------------------------------------------------------- */
+
+/* Copy whole pages: for k < n, page src[k] -> page dst[k] of KV-cache group
+ * `group` in every layer's K and V cache (a page is shared until one of its
+ * owners writes to it; then that owner takes a copy).
+ *   src, dst     HOST int32[n], each in [0, the group's pool) and not the null
+ *                block; no page is twice a destination, or both a source and a
+ *                destination (a source may feed several destinations)
+ *   k_cache, v_cache  HOST arrays of num_layers DEVICE pointers, 16-byte aligned;
+ *                page m starts at m * block_bytes (multiple of 16)
+ * On the handle's stream; staged deltas are flushed first.  Errors: EINVAL, ERANGE
+ * (bad page id), ESTATE (the stream is being captured), EHIP. */
+int ric_copy_blocks(ric_batch* b, int32_t group, int32_t n, const int32_t* src, const int32_t* dst,
+                    void* const* k_cache, void* const* v_cache, int32_t num_layers, int64_t block_bytes);
+
+/* ric_copy_blocks that also renames: every entry src[k] in the live requests'
+ * block tables of the group becomes dst[k] (compaction, defragmenting a pool:
+ * ric_compact_plan gives the pairs).  src must be distinct.  The caller's own
+ * accounts follow the same pairs.  Slots compiled before the move name the old
+ * pages: schedule and compile again.  The live rows must be condensed (ESTATE).
+ * num_layers may be 0 (tables only). */
+int ric_move_blocks(ric_batch* b, int32_t group, int32_t n, const int32_t* src, const int32_t* dst,
+                    void* const* k_cache, void* const* v_cache, int32_t num_layers, int64_t block_bytes);
+
+/* How many entries of the live requests' tables name each page of the group:
+ * dev_refs DEVICE int32[the group's pool]; pages of count 0 are free.  On the
+ * handle's stream, nothing is read back; staged deltas are flushed first.  The
+ * rows must be condensed (ESTATE). */
+int ric_block_refs(ric_batch* b, int32_t group, int32_t* dev_refs);
+
+/* A new request `child_id` that continues `parent_id`'s history: the first
+ * num_tokens tokens, the same prompt length (num_prompt <= num_tokens <= the
+ * parent's history), num_computed <= num_tokens of them in the cache.  Its block
+ * table (group 0) is the parent's first num_computed / B pages, shared, then
+ * new_blocks[0..num_new).  If num_computed % B rows of a further page are
+ * valid, num_new must be >= 1 and those rows of the parent's page are copied
+ * into new_blocks[0] in every layer's caches (row_bytes per token, multiple of
+ * 16; num_layers may be 0, then no rows are copied).  The parent's tokens and
+ * page ids are read on the device; its K/V must have been written on the handle's
+ * stream.  sampling NULL: the parent's values.  Other groups' rows start empty.
+ * Errors: ENOENT, EEXIST, EFULL, ERANGE, EINVAL, ESTATE (captured stream). */
+int ric_fork_request(ric_batch* b, uint64_t parent_id, uint64_t child_id, int32_t num_tokens, int32_t num_computed,
+                     const int32_t* new_blocks, int32_t num_new, void* const* k_cache, void* const* v_cache,
+                     int32_t num_layers, int32_t row_bytes, const ric_sampling* sampling, int32_t* out_row);
+
+/* Host only: the moves that compact a pool.  refs HOST int32[num_blocks] (> 0:
+ * in use); the k-th lowest free page other than null_block receives the k-th
+ * highest used one while the free page lies below it.  Writes src / dst (either
+ * may be NULL) and returns the count, or EINVAL. */
+int32_t ric_compact_plan(const int32_t* refs, int32_t num_blocks, int32_t null_block, int32_t* src, int32_t* dst);
+
 /* ---- host-only helpers (no device work) ----------------------------------- */
 
 /* Smallest of the n capture sizes >= num_tokens; num_tokens itself when it

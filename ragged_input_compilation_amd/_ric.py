@@ -35,6 +35,8 @@ class RicError(RuntimeError):
 RIC_MAX_KV_GROUPS, RIC_SLOTS_PER_TOKEN, RIC_SLOTS_NONE = 4, 0, 1
 RIC_FUSE_ALWAYS, RIC_FUSE_NEVER = 1, 2
 RIC_CHECK_SLOTS_NOALLOC_MAX_SLOTS = 1 << 25
+RIC_F16, RIC_BF16, RIC_F32 = 0, 1, 2
+RIC_MAX_TOP_LOGPROBS = 64
 
 
 class ric_config(ctypes.Structure):
@@ -72,6 +74,12 @@ class ric_spec_decode(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("logits_indices", "cu_num_logits", "target_logits_indices",
                                    "bonus_logits_indices", "draft_token_ids")] + \
                [("num_logits", ctypes.c_int32), ("num_draft_tokens", ctypes.c_int32)]
+
+
+class ric_attention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "num_heads", "num_kv_heads", "head_dim", "block_size")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", _vp), ("prefix_lens", _vp)]
 
 
 def _load():
@@ -129,7 +137,29 @@ def _load():
         "ric_check_step": (ctypes.c_int, [ctypes.POINTER(ric_config), ctypes.c_int32] + [_i32p] * 5 +
                            [ctypes.c_int32, ctypes.POINTER(ric_step)]),
     }
-    for name, (res, args) in sig.items():
+    # the operators around the step (ric_ops_host.cpp)
+    i32, i64, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    att = ctypes.POINTER(ric_attention)
+    pages = [_vp, i32, i32, _i32p, _i32p, ctypes.POINTER(_vp), ctypes.POINTER(_vp), i32, i64]
+    ops = {
+        "ric_paged_attention_workspace_bytes": (size, [att, i32, i32, i32, i32]),
+        "ric_paged_attention": (ctypes.c_int, [att, _vp, i64, _vp, _vp, i64, _vp, i64, i32, _vp, _vp, i32, i32, i32,
+                                               i32, _vp, i64, _vp, size, _vp, _vp]),
+        "ric_token_logprobs_workspace_bytes": (size, [i32, i32, i32]),
+        "ric_token_logprobs": (ctypes.c_int, [_vp, i32, i64, _vp, _vp, i32, i32, i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              size, _vp, _vp]),
+        "ric_copy_blocks": (ctypes.c_int, pages),
+        "ric_move_blocks": (ctypes.c_int, pages),
+        "ric_block_refs": (ctypes.c_int, [_vp, i32, _vp]),
+        "ric_fork_request": (ctypes.c_int, [_vp, ctypes.c_uint64, ctypes.c_uint64, i32, i32, _i32p, i32,
+                                            ctypes.POINTER(_vp), ctypes.POINTER(_vp), i32, i32,
+                                            ctypes.POINTER(ric_sampling), _i32p]),
+        "ric_compact_plan": (i32, [_i32p, i32, i32, _i32p, _i32p]),
+    }
+    if os.environ.get("RIC_LIBRARY"):
+        # a host-only build may hold the step's control plane alone
+        ops = {n: s for n, s in ops.items() if hasattr(lib, n)}
+    for name, (res, args) in {**sig, **ops}.items():
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args
@@ -396,6 +426,88 @@ def ric_check_slots_noalloc(slot_mapping: int, num_tokens: int, num_slots: int, 
                                       num_slots, _vp(dev_result or None), _vp(stream or None)))
 
 
+# ---- operators around the step -----------------------------------------------------
+
+def make_attention(**kw) -> ric_attention:
+    """Fields by name; alibi_slopes and prefix_lens are device addresses (0: none)."""
+    a = ric_attention()
+    for k, v in kw.items():
+        setattr(a, k, (v or None) if k in ("alibi_slopes", "prefix_lens") else v)
+    return a
+
+
+def ric_paged_attention_workspace_bytes(a: ric_attention, num_reqs: int, num_tokens: int, max_query_len: int,
+                                        max_seq_len: int) -> int:
+    return int(_lib.ric_paged_attention_workspace_bytes(ctypes.byref(a), num_reqs, num_tokens, max_query_len,
+                                                        max_seq_len))
+
+
+def ric_paged_attention(a: ric_attention, q: int, k_cache: int, v_cache: int, num_blocks: int, block_table: int,
+                        block_table_stride: int, block_table_width: int, query_start_loc: int, seq_lens: int,
+                        num_reqs: int, num_tokens: int, max_query_len: int, max_seq_len: int, out: int,
+                        q_stride: int = 0, out_stride: int = 0, workspace: int = 0, workspace_bytes: int = 0,
+                        dev_status: int = 0, stream: int = 0) -> None:
+    _err(_lib.ric_paged_attention(ctypes.byref(a), q or None, q_stride, k_cache or None, v_cache or None, num_blocks,
+                                  block_table or None, block_table_stride, block_table_width, query_start_loc or None,
+                                  seq_lens or None, num_reqs, num_tokens, max_query_len, max_seq_len, out or None,
+                                  out_stride, workspace or None, workspace_bytes, dev_status or None, stream or None))
+
+
+def ric_token_logprobs_workspace_bytes(max_rows: int, vocab: int, top_k: int) -> int:
+    return int(_lib.ric_token_logprobs_workspace_bytes(max_rows, vocab, top_k))
+
+
+def ric_token_logprobs(logits: int, dtype: int, targets: int, max_rows: int, vocab: int, top_k: int, logprob: int,
+                       rank: int, entropy: int, top_ids: int, top_logprobs: int, row_stride: int = 0,
+                       dev_count: int = 0, workspace: int = 0, workspace_bytes: int = 0, dev_status: int = 0,
+                       stream: int = 0) -> None:
+    _err(_lib.ric_token_logprobs(logits or None, dtype, row_stride, targets or None, dev_count or None, max_rows, vocab,
+                                 top_k, logprob or None, rank or None, entropy or None, top_ids or None,
+                                 top_logprobs or None, workspace or None, workspace_bytes, dev_status or None,
+                                 stream or None))
+
+
+def _page_args(src, dst, k_cache_ptrs, v_cache_ptrs):
+    s, sp = _i32(src)
+    d, dp = _i32(dst)
+    if s.shape != d.shape or s.ndim != 1:
+        raise ValueError("src and dst differ in length")
+    if len(k_cache_ptrs) != len(v_cache_ptrs):
+        raise ValueError("pointer lists differ in length")
+    L = len(k_cache_ptrs)
+    kc, vc = ((_vp * max(L, 1))(*[_vp(x) for x in lst]) for lst in (k_cache_ptrs, v_cache_ptrs))
+    return (s, d, kc, vc), (s.shape[0], sp, dp, ctypes.cast(kc, ctypes.POINTER(_vp)),
+                            ctypes.cast(vc, ctypes.POINTER(_vp)), L)
+
+
+def ric_copy_blocks(h: int, src, dst, k_cache_ptrs, v_cache_ptrs, block_bytes: int, group: int = 0) -> None:
+    keep, a = _page_args(src, dst, k_cache_ptrs, v_cache_ptrs)
+    _err(_lib.ric_copy_blocks(_vp(h), group, *a, block_bytes))
+
+
+def ric_move_blocks(h: int, src, dst, k_cache_ptrs, v_cache_ptrs, block_bytes: int, group: int = 0) -> None:
+    keep, a = _page_args(src, dst, k_cache_ptrs, v_cache_ptrs)
+    _err(_lib.ric_move_blocks(_vp(h), group, *a, block_bytes))
+
+
+def ric_block_refs(h: int, dev_refs: int, group: int = 0) -> None:
+    _err(_lib.ric_block_refs(_vp(h), group, _vp(dev_refs or None)))
+
+
+def ric_fork_request(h: int, parent_id: int, child_id: int, num_tokens: int, num_computed: int, new_blocks,
+                     k_cache_ptrs=(), v_cache_ptrs=(), row_bytes: int = 0, sampling=None) -> int:
+    blk, bp = _i32(new_blocks)
+    keep, a = _page_args([], [], k_cache_ptrs, v_cache_ptrs)
+    sp = None
+    if sampling is not None:
+        t, p, rp, k = sampling
+        sp = ctypes.byref(ric_sampling(t, p, rp, k))
+    row = ctypes.c_int32(-1)
+    _err(_lib.ric_fork_request(_vp(h), parent_id, child_id, num_tokens, num_computed, bp, blk.shape[0], *a[3:],
+                               row_bytes, sp, ctypes.byref(row)))
+    return row.value
+
+
 # ---- host-only helpers ----------------------------------------------------------
 
 def ric_padded_size(capture_sizes, num_tokens: int) -> int:
@@ -410,6 +522,14 @@ def ric_condense_plan(live):
     n = _err(_lib.ric_condense_plan(m.ctypes.data_as(_u8p), m.shape[0], holes.ctypes.data_as(_i32p),
                                     srcs.ctypes.data_as(_i32p)))
     return list(zip(holes[:n].tolist(), srcs[:n].tolist()))
+
+
+def ric_compact_plan(refs, null_block: int = 0):
+    """(src, dst) pages of the moves that compact a pool with these reference counts."""
+    r, rp = _i32(refs)
+    src, dst = np.zeros(max(r.shape[0], 1), np.int32), np.zeros(max(r.shape[0], 1), np.int32)
+    n = _err(_lib.ric_compact_plan(rp, r.shape[0], null_block, src.ctypes.data_as(_i32p), dst.ctypes.data_as(_i32p)))
+    return src[:n].copy(), dst[:n].copy()
 
 
 def ric_check_step(cfg: ric_config, num_computed, num_scheduled, num_prompt, num_tokens, num_blocks,

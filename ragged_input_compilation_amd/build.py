@@ -10,7 +10,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libric.so")
-SOURCES = [os.path.join(CSRC, "ric_kernels.hip"), os.path.join(CSRC, "ric_host.cpp")]
+SOURCES = [os.path.join(CSRC, n) for n in ("ric_kernels.hip", "ric_attention.hip", "ric_logprobs.hip", "ric_pages.hip",
+                                           "ric_host.cpp", "ric_ops_host.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -40,7 +40,7 @@ struct Layout {
     size_t off_tok, off_blk, off_scal, off_ids, off_pos, off_req, off_slot, off_qsl, off_seq,
         off_logits, off_sample, off_discard, off_dscal, off_pairs, off_cuk, off_samp_off, off_samp_idx,
         off_spec_logits, off_spec_target, off_spec_draft, off_spec_cu, off_spec_bonus, off_spec_d,
-        off_corr, off_staging, total;
+        off_corr, off_pages, off_staging, total;
     size_t staging_bytes;
     // KV-cache groups 1..groups-1 (index g): block tables and slot outputs
     int groups;
@@ -75,6 +75,7 @@ struct ric_batch {
     int32_t *d_spec_logits = nullptr, *d_spec_target = nullptr, *d_spec_draft = nullptr,
             *d_spec_cu = nullptr, *d_spec_bonus = nullptr, *d_spec_d = nullptr;
     int32_t* d_corr = nullptr;       // [3][max_num_reqs]: rows, sampler positions, draft counts
+    int32_t* d_pages = nullptr;      // [kMaxPagePairs][2]: page copies being made
     uint8_t* d_staging = nullptr;
 
     // pinned delta logs

@@ -129,6 +129,7 @@ Layout layout_of(const ric_config& c) {
     L.off_spec_bonus = take(R * 4);
     L.off_spec_d = take(R * 4);
     L.off_corr = take(R * 3 * 4);
+    L.off_pages = take((size_t)kMaxPagePairs * 2 * 4);
     L.groups = num_groups_of(c);
     for (int g = 1; g < L.groups; ++g) {
         L.xblk_stride[g] = round4(group_cap(c, g));
@@ -420,6 +421,7 @@ int ric_create(const ric_config* cfg, void* stream, void* workspace, size_t work
     b->d_spec_bonus = reinterpret_cast<int32_t*>(b->ws + L.off_spec_bonus);
     b->d_spec_d = reinterpret_cast<int32_t*>(b->ws + L.off_spec_d);
     b->d_corr = reinterpret_cast<int32_t*>(b->ws + L.off_corr);
+    b->d_pages = reinterpret_cast<int32_t*>(b->ws + L.off_pages);
     b->d_staging = b->ws + L.off_staging;
     for (int i = 0; i < 2; ++i) {
         void* p = nullptr;

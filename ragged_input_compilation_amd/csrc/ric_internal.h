@@ -30,6 +30,8 @@ __host__ __device__ inline int blocks_col(int g) { return g == 0 ? kNumBlocks : 
 constexpr int kMaxReqsLimit = 8000;       // compile LDS: 2R + 21 int32 (+ up to 128 slots) < 64 KiB
 constexpr int kMaxLayersPerLaunch = 32;   // K/V pointer sets passed by value
 constexpr int kNumDevScalars = 8;
+constexpr int kMaxPagePairs = 4096;       // page copies per launch (the pairs fit LDS)
+constexpr int kMaxTopLogprobs = 64;
 
 // One staged copy: n_words 32-bit words from the staging payload to dst.
 struct DeltaOp {
@@ -152,6 +154,87 @@ struct CorrectParams {
     int32_t n;
 };
 
+struct AttnParams {
+    const uint8_t* q;
+    uint8_t* out;
+    int64_t q_stride;             // bytes between tokens
+    int64_t out_stride;
+    const uint8_t* kc;            // [num_blocks][block_size][num_kv_heads][head_dim]
+    const uint8_t* vc;
+    const int32_t* table;
+    int64_t table_stride;         // entries between requests
+    const int32_t* qsl;           // [num_reqs + 1]
+    const int32_t* seq;           // [num_reqs]
+    const float* slopes;          // [num_heads] or null
+    const int32_t* prefix;        // [num_reqs] or null
+    int32_t* status;              // or null
+    int64_t num_blocks;
+    int32_t table_width;
+    int32_t num_reqs;
+    int32_t num_tokens;
+    int32_t max_q;
+    int32_t max_seq;
+    int32_t heads;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t block_size;
+    int32_t block_shift;          // log2(block_size) when a power of two, else -1
+    int32_t window;               // 0: none
+    float scale;
+    float cap;                    // 0: none
+    bool bf16;
+};
+
+struct LogprobParams {
+    const uint8_t* logits;
+    int64_t row_stride;           // bytes
+    const int32_t* targets;       // or null
+    const int32_t* dev_count;     // or null
+    float* logprob;
+    int32_t* rank;
+    float* entropy;               // or null
+    int32_t* top_ids;
+    float* top_logprobs;
+    int32_t* status;              // or null
+    int32_t max_rows;
+    int32_t vocab;
+    int32_t top_k;
+    int32_t dtype;
+};
+
+struct PageParams {
+    const uint8_t* kc[kMaxLayersPerLaunch];   // pointers first: one launch's layers
+    const uint8_t* vc[kMaxLayersPerLaunch];
+    const int32_t* pairs;         // [num_pairs][2] = (source, destination) page
+    int64_t block_bytes;
+    int32_t num_pairs;
+    int32_t num_layers;
+    // block tables that follow the move (rows 0: none); pairs sorted by source
+    int32_t* blocks;
+    const int32_t* num_blocks;    // device column
+    int64_t blk_stride;
+    int32_t rows;
+};
+
+struct ForkParams {
+    uint8_t* kc[kMaxLayersPerLaunch];
+    uint8_t* vc[kMaxLayersPerLaunch];
+    int32_t num_layers;
+    int32_t row_bytes;
+    int32_t block_size;
+    int32_t pool;
+    int32_t* tokens;
+    int64_t tok_stride;
+    int32_t* blocks;
+    int64_t blk_stride;
+    int32_t parent;               // rows
+    int32_t child;
+    int32_t num_tokens;           // history copied
+    int32_t num_shared;           // whole pages shared
+    int32_t tail_rows;            // valid rows of the parent's next page
+    int32_t tail_block;           // page that takes them
+};
+
 // Launchers (enqueue only; return the launch status).
 hipError_t launch_compile(const CompileParams& p, hipStream_t s);
 hipError_t launch_kv_scatter(const KVParams& p, int num_layers, hipStream_t s);
@@ -164,6 +247,16 @@ hipError_t launch_correct_computed(const CorrectParams& p, hipStream_t s);
 // dst_off[k] (int64, in int32 elements of the token table) <- src[src_idx[k]]
 hipError_t launch_append_sampled(int32_t* tokens, const int64_t* dst_off, const int32_t* src_idx,
                                  const int32_t* src, int32_t src_len, int32_t n, int32_t* err, hipStream_t s);
+
+hipError_t launch_page_copy(const PageParams& p, hipStream_t s);
+hipError_t launch_block_refs(const int32_t* blocks, int64_t blk_stride, const int32_t* num_blocks, int32_t rows,
+                             int32_t pool, int32_t* refs, hipStream_t s);
+hipError_t launch_fork(const ForkParams& p, bool rows, hipStream_t s);
+// Workspace bytes / launches of the attention and log-probability calls.
+size_t attention_workspace(const AttnParams& p);
+hipError_t launch_attention(const AttnParams& p, void* workspace, hipStream_t s);
+size_t logprobs_workspace(int32_t max_rows, int32_t vocab, int32_t top_k);
+hipError_t launch_logprobs(const LogprobParams& p, void* workspace, hipStream_t s);
 
 // Compile plus the K/V write of `num_layers` (<= kMaxLayersPerLaunch) layers
 // through the group-0 slots in one launch; only for rows the fused kernel

@@ -8,6 +8,7 @@ only sequences the calls: load the request history into the persistent batch
 layer, gather hidden rows."""
 from __future__ import annotations
 
+import contextlib
 import os
 from dataclasses import dataclass
 from typing import List, Optional
@@ -130,6 +131,14 @@ class Batch:
         dup, bad = self.slot_collisions(s)
         print(f"[ric] slot collisions {dup}, out-of-range slots {bad}", flush=True)
 
+    def block_table(self, group: int = 0) -> torch.Tensor:
+        """The handle's own block table of a KV-cache group, [max_num_reqs, stride]
+        int32 (entries past a row's count are stale): what an attention call reads."""
+        cols = ric.ric_get_columns(self.h)
+        stride = cols.group_block_stride[group]
+        n = self.cfg.max_num_reqs * stride
+        return _view_u8(self.workspace, cols.group_blocks[group], 4 * n).view(torch.int32).view(-1, stride)
+
     # inspection (tests) ------------------------------------------------------
     def device_i32(self, ptr: int, n: int) -> np.ndarray:
         """Copy n int32 values from a device address to the host (test use)."""
@@ -248,3 +257,186 @@ def gather(hidden: torch.Tensor, idx_ptr: int, dev_count_ptr: int, max_rows: int
                         idx_ptr, dev_count_ptr, max_rows, row_bytes, out.data_ptr(),
                         out.stride(0) * out.element_size(), dev_status,
                         current_stream() if stream is None else stream)
+
+
+# ---- operators around the step ------------------------------------------------------
+
+_DTYPE = {torch.float16: ric.RIC_F16, torch.bfloat16: ric.RIC_BF16, torch.float32: ric.RIC_F32}
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _allocating_on(stream: int):
+    """Context in which torch allocates for work on ``stream``."""
+    return contextlib.nullcontext() if stream == current_stream() else torch.cuda.stream(torch.cuda.ExternalStream(stream))
+
+
+def _attention(q, k_cache, scale=None, softcap=0.0, window=0, alibi_slopes=None, prefix_lens=None) -> ric.ric_attention:
+    if q.dtype not in (torch.float16, torch.bfloat16) or k_cache.dtype != q.dtype:
+        raise ValueError("q and the caches must be float16 or bfloat16, and alike")
+    return ric.make_attention(dtype=_DTYPE[q.dtype], num_heads=q.shape[1], num_kv_heads=k_cache.shape[2],
+                              head_dim=q.shape[2], block_size=k_cache.shape[1],
+                              scale=q.shape[2] ** -0.5 if scale is None else scale, softcap=softcap, window=window,
+                              alibi_slopes=_ptr(alibi_slopes), prefix_lens=_ptr(prefix_lens))
+
+
+def attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, num_reqs: int, max_query_len: int,
+                        max_seq_len: int) -> Optional[torch.Tensor]:
+    """A workspace for paged_attention calls of these bounds (None: none needed).
+    Calls that may run at the same time need one each."""
+    n = ric.ric_paged_attention_workspace_bytes(_attention(q, k_cache), num_reqs, q.shape[0], max_query_len, max_seq_len)
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    query_start_loc: torch.Tensor, seq_lens: torch.Tensor, max_query_len: int, max_seq_len: int,
+                    out: torch.Tensor, scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                    alibi_slopes: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, dev_status: int = 0) -> torch.Tensor:
+    """Attention of q [num_tokens, heads, head_dim] over the pages of each
+    request (ric_paged_attention), on the current stream.  k_cache, v_cache
+    [num_blocks, block_size, kv_heads, head_dim]; block_table [num_reqs, width]
+    int32; query_start_loc [num_reqs + 1], seq_lens [num_reqs] int32.  Without a
+    workspace one is allocated where the call needs it."""
+    a = _attention(q, k_cache, scale, softcap, window, alibi_slopes, prefix_lens)
+    n = seq_lens.shape[0]
+    if k_cache.shape != v_cache.shape or v_cache.dtype != q.dtype or k_cache.shape[3] != q.shape[2]:
+        raise ValueError("k_cache and v_cache must be [num_blocks, block_size, kv_heads, head_dim] of q's type")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must be like q")
+    for t in (q, out):
+        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+            raise ValueError("the heads of a token must be contiguous")
+    for t, k in ((query_start_loc, n + 1), (seq_lens, n), (prefix_lens, n)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != k or not t.is_contiguous()):
+            raise ValueError(f"query_start_loc [{n + 1}], seq_lens and prefix_lens [{n}] must be contiguous int32")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] < n or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [num_reqs, width] with contiguous rows")
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (q.shape[1],) or
+                                     not alibi_slopes.is_contiguous()):
+        raise ValueError("alibi_slopes must be contiguous float32 [heads]")
+    if workspace is None:
+        workspace = attention_workspace(q, k_cache, n, max_query_len, max_seq_len)
+    ric.ric_paged_attention(a, _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_table),
+                            max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
+                            _ptr(query_start_loc), _ptr(seq_lens), n, q.shape[0], max_query_len, max_seq_len, _ptr(out),
+                            q_stride=q.stride(0) * 2 if q.shape[0] > 1 else 0,
+                            out_stride=out.stride(0) * 2 if out.shape[0] > 1 else 0, workspace=_ptr(workspace),
+                            workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size(),
+                            dev_status=dev_status, stream=current_stream())
+    return out
+
+
+def step_attention(batch: "Batch", step: ric.ric_step, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   out: torch.Tensor, group: int = 0, workspace: Optional[torch.Tensor] = None, dev_status: int = 0,
+                   **kw) -> torch.Tensor:
+    """One layer's attention of a compiled step: q [num_tokens_padded, heads,
+    head_dim] over the caches its K/V rows were written to, through the handle's
+    own query_start_loc, seq_lens and block table.  Enqueued on the handle's
+    stream; ``kw``: scale, softcap, window, alibi_slopes, prefix_lens."""
+    a = _attention(q, k_cache, **kw)
+    cols = ric.ric_get_columns(batch.h)
+    if q.shape[0] != step.num_tokens_padded or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must hold the step's padded tokens")
+    if k_cache.shape != v_cache.shape or v_cache.dtype != q.dtype or k_cache.shape[3] != q.shape[2] or \
+            not (k_cache.is_contiguous() and v_cache.is_contiguous() and q.is_contiguous() and out.is_contiguous()):
+        raise ValueError("contiguous q, out and caches of one type are needed")
+    if workspace is None:
+        with _allocating_on(batch.stream):
+            workspace = attention_workspace(q, k_cache, step.num_reqs, step.max_query_len, step.max_seq_len)
+    ric.ric_paged_attention(a, _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], cols.group_blocks[group],
+                            cols.group_block_stride[group], cols.group_block_stride[group], step.query_start_loc,
+                            step.seq_lens, step.num_reqs, q.shape[0], step.max_query_len, step.max_seq_len, _ptr(out),
+                            workspace=_ptr(workspace),
+                            workspace_bytes=0 if workspace is None else workspace.numel(), dev_status=dev_status,
+                            stream=batch.stream)
+    return out
+
+
+@dataclass
+class Logprobs:
+    """Outputs of token_logprobs: [rows] float32, int32, float32; [rows, top_k]."""
+    logprob: torch.Tensor
+    rank: torch.Tensor
+    entropy: torch.Tensor
+    top_ids: torch.Tensor
+    top_logprobs: torch.Tensor
+    workspace: Optional[torch.Tensor]
+
+
+def alloc_logprobs(rows: int, vocab: int, top_k: int, device="cuda") -> Logprobs:
+    """Output and workspace tensors for token_logprobs calls of up to ``rows`` rows."""
+    f = lambda *s: torch.empty(s, dtype=torch.float32, device=device)
+    i = lambda *s: torch.empty(s, dtype=torch.int32, device=device)
+    n = ric.ric_token_logprobs_workspace_bytes(rows, vocab, top_k)
+    return Logprobs(f(rows), i(rows), f(rows), i(rows, top_k), f(rows, top_k),
+                    torch.empty(n, dtype=torch.uint8, device=device) if n else None)
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top_k: int = 0,
+                   out: Optional[Logprobs] = None, dev_count: int = 0, dev_status: int = 0) -> Logprobs:
+    """Log probability, rank, entropy and top_k alternatives of each row of
+    logits [rows, vocab] (ric_token_logprobs), on the current stream.  With
+    ``out`` the first ``rows`` rows of its tensors are written."""
+    if logits.dim() != 2 or logits.dtype not in _DTYPE or (logits.numel() and logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [rows, vocab] of float16, bfloat16 or float32 with contiguous rows")
+    rows, vocab = logits.shape
+    if targets is not None and (targets.dtype != torch.int32 or targets.shape != (rows,) or not targets.is_contiguous()):
+        raise ValueError("targets must be contiguous int32 [rows]")
+    if out is None:
+        out = alloc_logprobs(rows, vocab, top_k, logits.device)
+    elif out.logprob.shape[0] < rows or out.top_ids.shape[1] != top_k:
+        raise ValueError("out is too small, or of another top_k")
+    has = targets is not None
+    ric.ric_token_logprobs(_ptr(logits), _DTYPE[logits.dtype], _ptr(targets), rows, vocab, top_k,
+                           _ptr(out.logprob) if has else 0, _ptr(out.rank) if has else 0, _ptr(out.entropy),
+                           _ptr(out.top_ids) if top_k else 0, _ptr(out.top_logprobs) if top_k else 0,
+                           row_stride=logits.stride(0) * logits.element_size() if rows > 1 else 0, dev_count=dev_count,
+                           workspace=_ptr(out.workspace),
+                           workspace_bytes=0 if out.workspace is None else out.workspace.numel(),
+                           dev_status=dev_status, stream=current_stream())
+    return out
+
+
+def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor]):
+    for t in [*kc, *vc]:
+        if not t.is_contiguous() or t.shape != kc[0].shape or t.dtype != kc[0].dtype:
+            raise ValueError("the layers' caches must be contiguous and alike")
+    nbytes = kc[0][0].numel() * kc[0].element_size() if kc else 0
+    return [t.data_ptr() for t in kc], [t.data_ptr() for t in vc], nbytes
+
+
+def copy_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
+    """Page src[k] -> page dst[k] in every layer's caches [num_blocks, ...] (ric_copy_blocks)."""
+    k, v, n = _pages(kc, vc)
+    ric.ric_copy_blocks(batch.h, src, dst, k, v, n, group)
+
+
+def move_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
+    """copy_blocks, and the live requests' block tables follow (ric_move_blocks)."""
+    k, v, n = _pages(kc, vc)
+    ric.ric_move_blocks(batch.h, src, dst, k, v, n, group)
+
+
+def block_refs(batch: "Batch", group: int = 0) -> torch.Tensor:
+    """Table entries that name each page of the group's pool, int32 (ric_block_refs),
+    written on the handle's stream."""
+    c = batch.cfg
+    pool = c.num_kv_blocks if group == 0 or c.group_num_kv_blocks[group] <= 0 else c.group_num_kv_blocks[group]
+    with _allocating_on(batch.stream):
+        refs = torch.empty(pool, dtype=torch.int32, device=batch.workspace.device)
+    ric.ric_block_refs(batch.h, refs.data_ptr(), group)
+    return refs
+
+
+def fork_request(batch: "Batch", parent_id: int, child_id: int, num_tokens: int, num_computed: int, new_blocks,
+                 kc: List[torch.Tensor], vc: List[torch.Tensor], sampling=None) -> int:
+    """A new request over the parent's history, sharing its full pages (ric_fork_request)."""
+    k, v, n = _pages(kc, vc)
+    return ric.ric_fork_request(batch.h, parent_id, child_id, num_tokens, num_computed, new_blocks, k, v,
+                                n // batch.cfg.block_size, sampling)

@@ -1,0 +1,300 @@
+"""Attention over the paged cache against its definition in 64 bits: single
+tokens, chunks and both; head sizes, groups and page sizes; caps, biases,
+windows and prefixes; masks that leave nothing; values that no row may see; bad
+pages; strides, streams, graphs and caches past 4 GiB."""
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from tests.gpu_helpers import expected_step, replay_history
+from tests.ops_helpers import attention_inputs, attention_reference, check_attention
+
+pytestmark = pytest.mark.gpu
+
+DECODE = [(1, t) for t in (1, 2, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 300, 1000, 2049)]
+CHUNKS = [(1, 1), (7, 7), (5, 40), (1, 77), (64, 64), (65, 200), (130, 131), (33, 700), (1, 512), (200, 200)]
+SPEC = [(q, t) for q, t in ((1, 9), (2, 33), (3, 64), (4, 129), (5, 800), (8, 70))]
+
+
+@pytest.fixture(scope="module")
+def runner():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from ragged_input_compilation_amd import runner
+    return runner
+
+
+def call(runner, inp, *, scale, softcap=0.0, window=0, slopes=None, prefix=None, status=None, out=None, max_q=None,
+         max_seq=None, **kw):
+    max_q = max([a for a, _ in inp["lens"]] + [1]) if max_q is None else max_q
+    max_seq = max([t for _, t in inp["lens"]] + [1]) if max_seq is None else max_seq
+    out = torch.full_like(inp["q"], 77.0) if out is None else out
+    return runner.paged_attention(
+        inp["q"], inp["kc"], inp["vc"], inp["table"], inp["qsl"], inp["seq"], max_q, max_seq, out, scale=scale,
+        softcap=softcap, window=window,
+        alibi_slopes=None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device="cuda"),
+        prefix_lens=None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device="cuda"),
+        dev_status=0 if status is None else status.data_ptr(), **kw)
+
+
+def both(runner, inp, label="", **kw):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = call(runner, inp, status=status, **kw)
+    want, tol = attention_reference(inp, **kw)
+    n = want.shape[0]
+    check_attention(got[:n], want, tol, label)
+    assert (got[n:] == 77.0).all(), "rows behind the last request were written"
+    assert status.item() == 0
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,kv_heads,dim,block", [
+    (2, 2, 64, 16), (8, 1, 128, 16), (4, 2, 128, 5), (16, 2, 64, 1), (32, 1, 128, 64), (3, 1, 128, 24), (40, 1, 64, 16),
+    (2, 1, 8, 16), (3, 3, 40, 7), (6, 2, 80, 16), (4, 2, 96, 16), (2, 1, 192, 16), (4, 1, 256, 32), (5, 5, 248, 16)])
+@pytest.mark.parametrize("lens", ["decode", "chunks", "spec"])
+def test_shapes(runner, dtype, heads, kv_heads, dim, block, lens):
+    reqs = {"decode": DECODE, "chunks": CHUNKS, "spec": SPEC}[lens]
+    inp = attention_inputs(reqs, heads=heads, kv_heads=kv_heads, dim=dim, block=block, dtype=dtype, seed=dim + block,
+                           pad_tokens=3)
+    both(runner, inp, scale=dim ** -0.5)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 72])
+@pytest.mark.parametrize("lens", ["decode", "chunks", "spec"])
+@pytest.mark.parametrize("kw", [
+    dict(softcap=20.0), dict(window=1), dict(window=3), dict(window=64), dict(window=100), dict(window=100000),
+    dict(slopes=[0.5, 0.25, 0.125, 0.0625, 1.0, 0.01, 0.0, 0.3]), dict(prefix="half"), dict(prefix="all"),
+    dict(prefix="past", window=50), dict(softcap=5.0, window=37, slopes=[0.1] * 8, prefix="half")],
+    ids=lambda k: "-".join(f"{a}{'' if a == 'slopes' else b}" for a, b in k.items()))
+def test_masks_caps_and_biases(runner, dim, lens, kw):
+    reqs = {"decode": DECODE, "chunks": CHUNKS, "spec": SPEC}[lens]
+    kw = dict(kw)
+    if "prefix" in kw:
+        kw["prefix"] = [{"half": t // 2, "all": t, "past": t + 9}[kw["prefix"]] for _, t in reqs]
+    inp = attention_inputs(reqs, heads=8, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=5, scale_q=2.0)
+    both(runner, inp, scale=dim ** -0.5, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 24])
+def test_empty_requests_and_rows_that_see_nothing(runner, dim):
+    """Requests without tokens or keys among others, chunks that stand before
+    position 0 (more query tokens than the length): zeros, not NaN."""
+    reqs = [(0, 0), (1, 0), (0, 50), (3, 2), (1, 1), (70, 0), (0, 0), (90, 33), (2, 200), (0, 0)]
+    inp = attention_inputs(reqs, heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.float16, seed=1, pad_tokens=5)
+    got = both(runner, inp, scale=0.2)
+    assert (got[0] == 0).all()
+    both(runner, inp, scale=0.2, window=4, prefix=[t // 3 for _, t in reqs])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_behind_the_mask_never_arrive(runner, dim, value):
+    """Non-finite K and V rows at positions that only some rows of a chunk see:
+    the rows before them stay finite and right, the rows that see a non-finite
+    value do not pretend otherwise."""
+    reqs = [(40, 40), (130, 300), (3, 100), (1, 90), (5, 64)]
+    inp = attention_inputs(reqs, heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=2)
+    for i, j in ((0, 17), (0, 31), (1, 250), (1, 299), (2, 99), (4, 62)):
+        page = inp["table"][i, j // 16].long()
+        inp["vc"][page, j % 16, 0, 5] = value
+        inp["vc"][page, j % 16, 1, dim - 1] = value
+    both(runner, inp, scale=dim ** -0.5)
+    # behind a window, and keys that no row sees
+    both(runner, inp, scale=dim ** -0.5, window=20)
+    for i, j in ((1, 3), (3, 2)):
+        page = inp["table"][i, j // 16].long()
+        inp["kc"][page, j % 16] = value
+        inp["vc"][page, j % 16] = value
+    both(runner, inp, scale=dim ** -0.5, window=20)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 16])
+def test_pages_that_name_nothing_are_left_out(runner, dim):
+    reqs = [(1, 100), (1, 500), (80, 200), (5, 64)]
+    inp = attention_inputs(reqs, heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=3)
+    pool = inp["kc"].shape[0]
+    inp["table"][0, 2] = -1
+    inp["table"][1, 0] = pool
+    inp["table"][1, 20] = 2 ** 31 - 1
+    inp["table"][2, 5] = -2 ** 31
+    inp["table"][3, :] = pool + 5
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = call(runner, inp, scale=0.1, status=status)
+    want, tol = attention_reference(inp, scale=0.1)
+    check_attention(got, want, tol)
+    assert status.item() > 0
+    # an invisible bad page is not looked at
+    status.zero_()
+    inp2 = attention_inputs([(1, 300), (20, 300)], heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=4)
+    inp2["table"][:, :10] = -1
+    got = call(runner, inp2, scale=0.1, window=60, status=status)
+    want, tol = attention_reference(inp2, scale=0.1, window=60)
+    check_attention(got, want, tol)
+    assert status.item() == 0
+    # a length past the table's width
+    inp2["table"] = inp2["table"][:, 10:16].contiguous()
+    inp2["lens"] = [(1, 96), (20, 300)]
+    inp2["seq"] = torch.tensor([96, 300], dtype=torch.int32, device="cuda")
+    got = call(runner, inp2, scale=0.1, status=status)
+    want, tol = attention_reference(inp2, scale=0.1)
+    check_attention(got, want, tol)
+    assert status.item() > 0
+
+
+def test_a_request_longer_than_declared_is_left_alone(runner):
+    reqs = [(1, 30), (50, 60), (1, 40)]
+    for heads, dim in ((4, 128), (4, 24)):
+        inp = attention_inputs(reqs, heads=heads, kv_heads=1, dim=dim, block=16, dtype=torch.float16)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = call(runner, inp, scale=0.1, status=status, max_q=2)
+        want, tol = attention_reference(inp, scale=0.1)
+        assert (got[1:51] == 77.0).all() and status.item() > 0
+        for rows in (slice(0, 1), slice(51, 52)):
+            check_attention(got[rows], want[rows], tol[rows])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 48])
+def test_strided_rows_in_place_and_a_wider_table(runner, dim):
+    reqs = CHUNKS + SPEC
+    inp = attention_inputs(reqs, heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=7)
+    want, tol = attention_reference(inp, scale=0.1)
+    n = inp["q"].shape[0]
+    # q as the query part of a fused projection, out inside a wider buffer
+    fused = torch.randn((n, 8, dim), device="cuda").to(torch.bfloat16)
+    fused[:, :4] = inp["q"]
+    wide = torch.full((n, 6, dim), 5.0, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((len(reqs), inp["table"].shape[1] + 6), -1, dtype=torch.int32, device="cuda")
+    table[:, :inp["table"].shape[1]] = inp["table"]
+    strided = dict(inp, q=fused[:, :4], table=table[:, :inp["table"].shape[1]])
+    call(runner, strided, scale=0.1, out=wide[:, 2:])
+    check_attention(wide[:, 2:], want, tol)
+    assert (wide[:, :2] == 5.0).all()
+    # the output over the queries
+    q = inp["q"].clone()
+    got = call(runner, dict(inp, q=q), scale=0.1, out=q)
+    check_attention(got, want, tol)
+
+
+@pytest.mark.parametrize("reqs", [[(1, 20000)], [(1, 9001), (2, 50)], [(16, 6000)], [(130, 9000)], [(1, 700)] * 40])
+@pytest.mark.parametrize("dim,heads,kv_heads", [(128, 8, 1), (64, 4, 2), (128, 8, 8)])
+def test_long_axes_and_equal_bits(runner, reqs, dim, heads, kv_heads):
+    """Few rows over many keys (the work is split along the keys): right, for any
+    declared length, and the same bits each time."""
+    inp = attention_inputs(reqs, heads=heads, kv_heads=kv_heads, dim=dim, block=16, dtype=torch.bfloat16, seed=11)
+    a = both(runner, inp, scale=dim ** -0.5)
+    b = both(runner, inp, scale=dim ** -0.5)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    want, tol = attention_reference(inp, scale=dim ** -0.5)
+    for hint in (1, 100000):
+        check_attention(call(runner, inp, scale=dim ** -0.5, max_seq=hint), want, tol)
+
+
+def test_cache_past_4_gib(runner):
+    """Pages whose byte offsets need more than 32 bits."""
+    B, KH, D = 16, 8, 128
+    pool = (5 << 30) // (B * KH * D * 2)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    kc = torch.empty((pool, B, KH, D), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    lens = [(1, 100), (40, 90)]
+    ids = torch.tensor([[pool - 1 - 3 * k for k in range(7)], [1 + (pool // 7) * k for k in range(7)]])
+    for i in range(2):
+        for b in ids[i].tolist():
+            kc[b] = torch.randn((B, KH, D), generator=g, device="cuda").to(torch.bfloat16)
+            vc[b] = torch.randn((B, KH, D), generator=g, device="cuda").to(torch.bfloat16)
+    inp = dict(q=torch.randn((41, 16, D), generator=g, device="cuda").to(torch.bfloat16), kc=kc, vc=vc,
+               table=ids.to(torch.int32).cuda(), qsl=torch.tensor([0, 1, 41], dtype=torch.int32, device="cuda"),
+               seq=torch.tensor([100, 90], dtype=torch.int32, device="cuda"), lens=lens)
+    both(runner, inp, scale=D ** -0.5)
+
+
+@pytest.mark.parametrize("dim", [128, 40])
+def test_another_stream_and_replayed_graphs(runner, dim):
+    """Two captured calls with a workspace each replay with other lengths, in
+    turn with eager work, and equal the eager results."""
+    shapes = [[(1, 3000), (1, 50), (90, 400)], [(1, 2000), (1, 777), (80, 90)], [(1, 1), (1, 2999), (91, 91)]]
+    n = max(sum(q for q, _ in s) for s in shapes)
+    make = lambda s: attention_inputs(s, heads=8, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=len(s),
+                                      extra_blocks=500 - sum(-(-t // 16) for _, t in s), pad_tokens=n - sum(q for q, _ in s))
+    sets = [make(s) for s in shapes]
+    width = max(s["table"].shape[1] for s in sets)
+    for s in sets:
+        t = torch.full((3, width), -1, dtype=torch.int32, device="cuda")
+        t[:, :s["table"].shape[1]] = s["table"]
+        s["table"] = t
+    buf = {k: sets[0][k].clone() for k in ("q", "kc", "vc", "table", "qsl", "seq")}
+    buf["lens"] = shapes[0]
+    outs = [torch.zeros_like(buf["q"]) for _ in range(2)]
+    work = [runner.attention_workspace(buf["q"], buf["kc"], 3, 91, 3000) for _ in range(2)]
+    run = lambda k: call(runner, buf, scale=0.1, out=outs[k], workspace=work[k], max_q=91, max_seq=3000)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(0)
+    side.synchronize()
+    want, tol = attention_reference(sets[0], scale=0.1)
+    check_attention(outs[0][:want.shape[0]], want, tol, "side stream")
+    graphs = []
+    for k in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(k)
+        graphs.append(g)
+    for rep in range(2):
+        for s in sets:
+            for key in ("q", "kc", "vc", "table", "qsl", "seq"):
+                buf[key].copy_(s[key])
+            want, tol = attention_reference(s, scale=0.1)
+            for k in range(2):
+                outs[k].zero_()
+                graphs[k].replay()
+            torch.cuda.synchronize()
+            eager = call(runner, buf, scale=0.1, max_q=91, max_seq=3000)
+            m = want.shape[0]
+            for k in range(2):
+                check_attention(outs[k][:m], want, tol, f"replay {rep}")
+                assert torch.equal(outs[k][:m].view(torch.int16), eager[:m].view(torch.int16))
+
+
+@pytest.mark.parametrize("name", ["worked_example", "mixed", "decode_heavy"])
+def test_a_compiled_step_attends_to_what_it_wrote(runner, name):
+    """Compile, K/V write and attention in a row: the queries see the cached
+    context and the rows that this step wrote, through the handle's own arrays;
+    padding rows stay as they were."""
+    w = workloads.get(name)
+    b = runner.Batch(runner.config_of(w))
+    b.load_history(w)
+    ref, order = replay_history(w)
+    b.schedule_from(w, order)
+    exp = expected_step(w, ref)
+    n_pad = exp["n_pad"]
+    kc, vc = runner.alloc_caches(w, 1)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for c in (kc[0], vc[0]):
+        c.copy_(torch.randn(c.shape, generator=g, device="cuda", dtype=c.dtype))
+    k, v = runner.alloc_sources(w, n_pad, seed=3, num_layers=1)
+    step = runner.compile_and_cache(b, n_pad, runner.KVSet(k, v, kc, vc, w.row_bytes, w.num_kv_blocks * w.block_size))
+    heads = 4 * w.kv_heads
+    q = torch.randn((n_pad, heads, w.head_dim), generator=g, device="cuda", dtype=kc[0].dtype)
+    out = torch.full_like(q, 3.0)
+    runner.step_attention(b, step, q, kc[0], vc[0], out)
+    rows = ref.step_rows()
+    pick = list(range(len(rows))) if name == "worked_example" else list(range(0, len(rows), 9))
+    qsl = exp["query_start_loc"]
+    lens = [(r.num_scheduled, r.num_computed + r.num_scheduled) for r in rows]
+    for i in pick:
+        n, t = lens[i]
+        if t > 4500:
+            continue
+        table = torch.tensor([rows[i].blocks], dtype=torch.int32, device="cuda")
+        one = dict(q=q[qsl[i]:qsl[i + 1]], kc=kc[0], vc=vc[0], table=table, lens=[(n, t)])
+        if n > 600:
+            one["q"] = one["q"][:, ::8].contiguous()
+            one["kc"], one["vc"] = kc[0][:, :, ::2], vc[0][:, :, ::2]
+        want, tol = attention_reference(one, scale=w.head_dim ** -0.5)
+        got = out[qsl[i]:qsl[i + 1]]
+        check_attention(got[:, ::8] if n > 600 else got, want, tol, f"request {i}")
+    assert (out[exp["num_actual_tokens"]:] == 3.0).all()
+    b.close()
