@@ -220,48 +220,30 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
     }
 
     // page id of the lane's two keys (16 s + c16) of a tile; -1 names nothing
-    auto page_of = [&](int j0, int s) -> int {
-        const int j = j0 + 16 * s + c16;
-        if (j >= end) return -1;
+    auto page_of = [&](int j) -> int {
         const int blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
-        return blk < p.table_width ? table[blk] : -1;
+        return j < end && blk < p.table_width ? table[blk] : -1;
     };
+    // A tile's K and V, requested without branches: a key without a page reads
+    // the cache's first row instead, and is masked (K) or cleared (V) later.
     u32x4 kr[2][DC], vr[2][DC];
-    auto load_tile = [&](int j0, const int id[2]) -> uint32_t {
-        bool ok[2];
-        int64_t off[2];
+    auto load_tile = [&](int j0, int id0, int id1) -> uint32_t {
+        uint64_t has[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int j = j0 + 16 * s + c16;
+            const int j = j0 + 16 * s + c16, id = s == 0 ? id0 : id1;
             const int blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
-            ok[s] = j < end && (uint32_t)id[s] < (uint64_t)p.num_blocks;
-            off[s] = ((int64_t)id[s] * p.block_size + (j - blk * p.block_size)) * row_bytes;
+            const bool ok = (uint32_t)id < (uint64_t)p.num_blocks;
+            const int64_t off = ok ? ((int64_t)id * p.block_size + (j - blk * p.block_size)) * row_bytes : 0;
+            has[s] = __ballot(ok);
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+                const int64_t at_piece = EXACT || c * 32 + g * 8 < dim ? off + c * 64 : off - g * 16;
+                kr[s][c] = *reinterpret_cast<const u32x4*>(kbase + at_piece);
+                vr[s][c] = *reinterpret_cast<const u32x4*>(vbase + at_piece);
+            }
         }
-        const uint64_t b0 = __ballot(ok[0]), b1 = __ballot(ok[1]);
-        if (EXACT && b0 == ~0ull && b1 == ~0ull) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int c = 0; c < DC; ++c)
-                    kr[s][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(kbase + off[s] + c * 64));
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int c = 0; c < DC; ++c)
-                    vr[s][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(vbase + off[s] + c * 64));
-        } else {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int c = 0; c < DC; ++c) {
-                    kr[s][c] = vr[s][c] = u32x4{0, 0, 0, 0};
-                    if (ok[s] && (EXACT || c * 32 + g * 8 < dim)) {
-                        kr[s][c] = *reinterpret_cast<const u32x4*>(kbase + off[s] + c * 64);
-                        vr[s][c] = *reinterpret_cast<const u32x4*>(vbase + off[s] + c * 64);
-                    }
-                }
-        }
-        return (uint32_t)(b0 & 0xffff) | (uint32_t)(b1 & 0xffff) << 16;
+        return (uint32_t)(has[0] & 0xffff) | (uint32_t)(has[1] & 0xffff) << 16;
     };
     // 16-byte piece c of row r in LDS; the pieces of neighbouring rows are turned
     // against each other, so that a column of 16 rows touches every bank
@@ -270,12 +252,13 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
     const int ntiles = (end - begin + kKeyTile - 1) / kKeyTile;
     int t = w;
     uint32_t have = 0;
-    int id[2], next[2] = {-1, -1};
+    int next0 = -1, next1 = -1;
     if (t < ntiles) {
-        const int j0 = begin + t * kKeyTile;
-        for (int s = 0; s < 2; ++s) id[s] = page_of(j0, s);
-        for (int s = 0; s < 2; ++s) next[s] = page_of(j0 + 4 * kKeyTile, s);
-        have = load_tile(j0, id);
+        const int j = begin + t * kKeyTile + c16;
+        const int id0 = page_of(j), id1 = page_of(j + 16);
+        next0 = page_of(j + 4 * kKeyTile);
+        next1 = page_of(j + 4 * kKeyTile + 16);
+        have = load_tile(j - c16, id0, id1);
     }
     bool bad_page = false;
     for (; t < ntiles; t += 4) {
@@ -287,14 +270,25 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
             for (int s = 0; s < 2; ++s) {
                 sc[b][s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < DC; ++c) sc[b][s] = mfma16<BF16>(kr[s][c], q[b][c], sc[b][s]);
+                for (int c = 0; c < DC; ++c) {
+                    const uint32_t in = EXACT || c * 32 + g * 8 < dim ? ~0u : 0u;     // 0 past the head, not NaN
+                    sc[b][s] = mfma16<BF16>(kr[s][c] & in, q[b][c], sc[b][s]);
+                }
             }
-        bool odd = false;                        // a non-finite V element in the lane's pieces
+        const uint32_t mask = have;
+        if (mask != ~0u) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t keep = (mask >> (16 * s + c16) & 1) ? ~0u : 0u;
+#pragma unroll
+                for (int c = 0; c < DC; ++c) vr[s][c] &= keep;
+            }
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int c = 0; c < DC; ++c) *reinterpret_cast<u32x4*>(my + at(16 * s + c16, c * 4 + g)) = vr[s][c];
-        const uint32_t mask = have;
+            for (int c = 0; c < DC; ++c)
+                if (EXACT || c * 32 + g * 8 < dim) *reinterpret_cast<u32x4*>(my + at(16 * s + c16, c * 4 + g)) = vr[s][c];
         const uint32_t inside = end - j0 >= 32 ? ~0u : (1u << (end - j0)) - 1u;
         bad_page |= (mask & inside) != inside;
         // Every row sees every key of the tile, unless the tile lies past the
@@ -305,17 +299,16 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
         if (!clear) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                odd = false;
+                bool odd = false;                // a non-finite element in the lane's pieces of V
 #pragma unroll
-                for (int c = 0; c < DC; ++c) odd |= non_finite<BF16>(vr[s][c]);
+                for (int c = 0; c < DC; ++c) odd |= (EXACT || c * 32 + g * 8 < dim) && non_finite<BF16>(vr[s][c]);
                 odd_keys[s] = __ballot(odd);
             }
         }
         if (t + 4 < ntiles) {
-            id[0] = next[0];
-            id[1] = next[1];
-            have = load_tile(j0 + 4 * kKeyTile, id);
-            for (int s = 0; s < 2; ++s) next[s] = page_of(j0 + 8 * kKeyTile, s);
+            have = load_tile(j0 + 4 * kKeyTile, next0, next1);
+            next0 = page_of(j0 + 8 * kKeyTile + c16);
+            next1 = page_of(j0 + 8 * kKeyTile + c16 + 16);
         }
         u32x4 pr[NB];
         uint32_t sees[NB];                        // the lane's row sees its key 16 s + 4 g + e: bit 16 s + e
@@ -387,14 +380,10 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
                     const uint32_t one = step == 0 ? 0u : todo & (0u - todo);
                     if (step > 0) todo &= todo - 1;
                     const uint32_t keys = step == 0 ? ~odd_tile : one;
-                    u32x4 part_v = vt;
-                    uint32_t mine = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (keys >> (16 * (e >> 2) + 4 * g + (e & 3)) & 1) mine |= 1u << e;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        part_v[k] &= ((mine >> (2 * k) & 1) ? 0xffffu : 0u) | ((mine >> (2 * k + 1) & 1) ? 0xffff0000u : 0u);
+                    // the lane's eight keys, as masks of the four words
+                    const uint32_t lo4 = keys >> (4 * g), hi4 = keys >> (16 + 4 * g);
+                    auto pair = [](uint32_t two) { return ((two & 1) ? 0xffffu : 0u) | ((two & 2) ? 0xffff0000u : 0u); };
+                    const u32x4 part_v = vt & u32x4{pair(lo4), pair(lo4 >> 2), pair(hi4), pair(hi4 >> 2)};
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         const f32x4 add = mfma16<BF16>(part_v, pr[b], f32x4{0.f, 0.f, 0.f, 0.f});
