@@ -485,7 +485,7 @@ int ric_check_slots_noalloc(const int32_t* slot_mapping, int32_t num_tokens, con
 /* What an attention layer is, independent of the step. */
 typedef struct {
     int32_t dtype;                /* RIC_F16 or RIC_BF16: q, caches and out                       */
-    int32_t num_heads;            /* query heads, a multiple of num_kv_heads: query head h reads
+    int32_t num_heads;            /* query heads (<= 512), a multiple of num_kv_heads: query head h reads
                                      K/V head h / (num_heads / num_kv_heads)                      */
     int32_t num_kv_heads;
     int32_t head_dim;             /* multiple of 8, 8..256                                        */
@@ -536,7 +536,7 @@ typedef struct {
  *                (two streams, two graphs) need one each
  * Everything is read on the device, so a captured call replays with new counts
  * as long as num_reqs, num_tokens and max_query_len still bound them.  Runs on the
- * current device.  num_tokens <= 2^22.  Equal inputs give equal bits.  Errors:
+ * current device.  num_tokens <= 2^22, num_reqs <= 65535.  Equal inputs give equal bits.  Errors:
  * EINVAL (shapes, strides, alignment, NULL, workspace too small), EHIP. */
 size_t ric_paged_attention_workspace_bytes(const ric_attention* a, int32_t num_reqs, int32_t num_tokens,
                                            int32_t max_query_len, int32_t max_seq_len);  /* 0 also on EINVAL */

@@ -59,6 +59,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <bool BF16>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -69,19 +70,17 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 template <bool BF16>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <bool BF16>
 __device__ __forceinline__ u32x4 round8(f32x8 x) {
     if constexpr (BF16) return __builtin_bit_cast(u32x4, __builtin_convertvector(x, bf16x8));
     else return __builtin_bit_cast(u32x4, __builtin_convertvector(x, f16x8));
-}
-
-// Any 16-bit value of the four words that is infinite or NaN (exponent all ones).
-template <bool BF16>
-__device__ __forceinline__ bool non_finite(u32x4 x) {
-    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) bad |= (x[k] & e) == e || ((x[k] >> 16) & e) == e;
-    return bad;
 }
 
 // Four 16-bit elements of one column from four consecutive rows: among each 16
@@ -90,6 +89,27 @@ __device__ __forceinline__ bool non_finite(u32x4 x) {
 __device__ __forceinline__ uint2 read_transposed(const uint8_t* lds) {
     typedef s16x4 __attribute__((address_space(3)))* lds_ptr;
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds)));
+}
+
+// Set where one of the eight 16-bit values is infinite or NaN (exponent all
+// ones: adding its lowest bit carries into the sign's place).
+template <bool BF16>
+__device__ __forceinline__ uint32_t odd_bits(u32x4 x) {
+    constexpr uint32_t e = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
+    uint32_t f = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f |= (x[k] & e) + one;
+    return f & 0x80008000u;
+}
+
+// Across the two halves of a wave, result in every lane.
+__device__ __forceinline__ float max_across32(float x) {
+    auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_across32(float x) {
+    auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Reductions across the four 16-lane groups of a wave, result in every lane.
@@ -301,7 +321,7 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
             for (int s = 0; s < 2; ++s) {
                 bool odd = false;                // a non-finite element in the lane's pieces of V
 #pragma unroll
-                for (int c = 0; c < DC; ++c) odd |= (EXACT || c * 32 + g * 8 < dim) && non_finite<BF16>(vr[s][c]);
+                for (int c = 0; c < DC; ++c) odd |= (EXACT || c * 32 + g * 8 < dim) && odd_bits<BF16>(vr[s][c]) != 0;
                 odd_keys[s] = __ballot(odd);
             }
         }
@@ -493,91 +513,317 @@ __global__ __launch_bounds__(256) void join_rows_kernel(AttnParams p, Partial pa
 }
 
 // ---------------------------------------------------------------------------
-// Any head size: one wave per (token, head).  A lane scores one key of a group
-// of 64 (its K row in 16-byte pieces against the query in LDS), then the wave
-// adds the group's V rows, each lane holding up to four output columns.
+// Many query rows (chunks).  Bound by the matrix products and the exponentials
+// between them.
+//
+// The n x G rows of a request's K/V head (row R: token R / G, head R % G, so that
+// neighbouring rows share positions and the tile's keys) are cut into tiles of
+// 128; a workgroup takes one tile, each of its four waves 32 rows, and walks the
+// keys in tiles of KT that all four share through LDS.  Tile x of the grid
+// belongs to the last request i with start_i = qsl[i] * G / 128 + i <= x: starts
+// that far apart hold every request's tiles, and need no prefix sum.
+//   S^T = K Q^T and O^T = V^T P^T on 32 x 32 x 16 products, as in the few-rows
+//   kernel: a lane's column is one query row, P^T is S^T rounded in place, V is
+//   read back from LDS transposed.  The other 16 keys of a row sit in lane ^ 32.
+//   K and V go from memory to LDS without registers (16 bytes per lane, the next
+//   tile while this one is computed); the lanes of a load pick which piece of
+//   which row they fetch, which turns rows against each other (no bank is hit
+//   more often than the access needs) and sends keys without a page to a zero.
+//   The maximum a row is scaled by is only raised when a new one exceeds it by
+//   more than 2^8, so most tiles leave the 64 accumulators untouched.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void attention_any_kernel(AttnParams p, int row_limit) {
-    __shared__ float qs[4][256];
-    __shared__ float ps[4][64];
-    __shared__ int64_t rows[4][64];
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int t = blockIdx.x, h = blockIdx.y * 4 + w;
-    if (h >= p.heads) return;
-    const int i = request_of(p.qsl, p.num_reqs, t);
-    if (i < 0) return;
-    const int first = p.qsl[i], n = p.qsl[i + 1] - first, seq = p.seq[i];
-    if (n > p.max_q) {
-        if (lane == 0 && t == first) raise(p.status);
+__device__ const u32x4 kZeroPiece = {0, 0, 0, 0};
+
+constexpr int kRowTile = 128;
+
+template <int DP>
+struct ChunkShape {
+    static constexpr int KT = DP <= 128 ? 64 : 32;         // keys per tile
+    static constexpr int KB = KT / 32;
+    static constexpr int CPR = DP / 8;                     // 16-byte pieces per row
+    static constexpr int TILE = KT * DP * 2;               // bytes of one K or V tile
+    static constexpr int LOADS = TILE / (4 * 1024);        // loads of 1 KiB per wave
+    // Where piece c of row r lies in its row.  A transposed read takes four
+    // neighbouring pieces of eight neighbouring rows, a K read one or two pieces
+    // of 32: both spread over all 256 bytes of banks.
+    __device__ static int turn(int r) {
+        if constexpr (DP == 64) return ((r >> 1 & 1) << 2) | (r >> 2 & 3);
+        else return ((r & 3) << 2) | (r >> 2 & 3);
+    }
+};
+
+// Copies 16 bytes per lane from memory to LDS at `lds` + 16 * lane.  Complete
+// after s_waitcnt vmcnt(0).  Written as text because the compiler, given its own
+// form, waits for the load in flight before every read of the other tile.  It
+// writes no register; M0, which holds the LDS address, is left as it was.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const uint8_t* src) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+}
+
+template <int DP, bool BF16, bool EXACT, bool FEAT>
+__global__ __launch_bounds__(256, 2) void attention_chunk_kernel(AttnParams p, int row_limit) {
+    using Shape = ChunkShape<DP>;
+    constexpr int KT = Shape::KT, KB = Shape::KB, CPR = Shape::CPR, TILE = Shape::TILE;
+    constexpr int QS = DP / 16, DB = DP / 32;
+    // [2][K, V] tiles from offset 0 (a load to LDS reaches 64 KiB), then a flag: a
+    // page that names nothing was met
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + 16];
+    int& gap = *reinterpret_cast<int*>(lds + 4 * TILE);
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, h32 = lane >> 5, c32 = lane & 31;
+    const int kvh = blockIdx.x % p.kv_heads;
+    const int x = gridDim.x / p.kv_heads - 1 - blockIdx.x / p.kv_heads;
+    const int G = p.heads / p.kv_heads;
+    auto start = [&](int i) { return (int)((int64_t)p.qsl[i] * G / kRowTile) + i; };
+    int i = 0;
+    for (int hi = p.num_reqs - 1; i < hi;) {
+        const int mid = (i + hi + 1) >> 1;
+        if (start(mid) <= x) i = mid; else hi = mid - 1;
+    }
+    const Span sp = span_of(p, i, 1, 1, 1);
+    const int row0 = (x - start(i)) * kRowTile, rows = sp.n * G;
+    if (row0 < 0 || row0 >= rows || rows <= row_limit) return;
+    if (sp.n > p.max_q) {
+        if (threadIdx.x == 0 && row0 == 0 && kvh == 0) raise(p.status);
         return;
     }
-    if (n * (p.heads / p.kv_heads) <= row_limit) return;
-    const int pos = seq - n + (t - first);
-    const int pre = p.prefix != nullptr ? p.prefix[i] : 0;
-    const int end = min(seq, max(pos + 1, pre));
-    const int begin = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
-    const float slope = p.slopes != nullptr ? p.slopes[h] : 0.f;
-    const int kvh = h / (p.heads / p.kv_heads);
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q + (int64_t)t * p.q_stride) + (int64_t)h * p.dim;
-    for (int d = lane; d < p.dim; d += 64) qs[w][d] = from_bits16(q[d], p.bf16);
-    const int64_t row_bytes = (int64_t)p.kv_heads * p.dim * 2;
+    const int dim = EXACT ? DP : p.dim;
+    const int64_t row_bytes = (int64_t)p.kv_heads * dim * 2;
     const int32_t* table = p.table + (int64_t)i * p.table_stride;
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = begin; j0 < end; j0 += 64) {
-        const int j = j0 + lane;
-        float s = -INFINITY;
-        bool bad = false;
-        int64_t at = -1;
-        if (j < end) {
-            const int b = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
-            const int64_t id = b < p.table_width ? table[b] : -1;
-            if (id < 0 || id >= p.num_blocks) {
-                bad = true;
-            } else {
-                at = (id * p.block_size + (j - b * p.block_size)) * row_bytes + (int64_t)kvh * p.dim * 2;
-                float dot = 0.f;
-                for (int d = 0; d < p.dim; d += 8) {
-                    const u32x4 k = *reinterpret_cast<const u32x4*>(p.kc + at + d * 2);
+    const uint8_t* kbase = p.kc + (int64_t)kvh * dim * 2;
+    const uint8_t* vbase = p.vc + (int64_t)kvh * dim * 2;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int pre = min(sp.pre, sp.seq);
+
+    // the wave's 32 rows, one per lane column
+    const int r = row0 + w * 32 + c32;
+    const bool in = r < rows;
+    const int tok = in ? r / G : 0, head = kvh * G + (in ? r - tok * G : 0);
+    const int pos = sp.seq - sp.n + (in ? tok : (rows - 1) / G);
+    const bool flip = !FEAT && p.scale < 0.f;    // a negative scale turns the queries' signs: exact
+    u32x4 q[QS];
+    {
+        const uint8_t* src = p.q + (int64_t)(sp.first + tok) * p.q_stride + (int64_t)head * dim * 2 + h32 * 16;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dot = fmaf(from_bits16(k[e] & 0xffffu, p.bf16), qs[w][d + 2 * e], dot);
-                        dot = fmaf(from_bits16(k[e] >> 16, p.bf16), qs[w][d + 2 * e + 1], dot);
-                    }
-                }
-                s = dot * p.scale;
-                if (p.cap > 0.f) s = p.cap * tanh_f32(s / p.cap);
-                s -= slope * fabsf((float)(pos - j));
+        for (int s = 0; s < QS; ++s) {
+            q[s] = u32x4{0, 0, 0, 0};
+            if (in && (EXACT || s * 16 + h32 * 8 < dim)) q[s] = *reinterpret_cast<const u32x4*>(src + s * 32);
+            if (flip) q[s] ^= 0x80008000u;
+        }
+    }
+    // scores in units of log2: x = c s (FEAT: x computed in full, c = 1)
+    const float c = FEAT ? 1.f : fabsf(p.scale) * kLog2e;
+    const float slope = FEAT && p.slopes != nullptr && in ? p.slopes[head] * kLog2e : 0.f;
+
+    // the keys that the tile's rows can see
+    const int p_first = sp.seq - sp.n + row0 / G, p_last = sp.seq - sp.n + min(rows - 1, row0 + kRowTile - 1) / G;
+    const int key_end = min(sp.seq, max(p_last + 1, pre));
+    const int key_begin = p.window > 0 ? max(0, p_first + 1 - p.window) / KT * KT : 0;
+    const int ntiles = key_end > key_begin ? (key_end - key_begin + KT - 1) / KT : 0;
+    const int p_wave = __builtin_amdgcn_readfirstlane(sp.seq - sp.n + min(rows - 1, row0 + w * 32) / G);
+    const int p_wave_last = __builtin_amdgcn_readfirstlane(sp.seq - sp.n + min(rows - 1, row0 + w * 32 + 31) / G);
+
+    // This lane's part of the tile loads: pieces lane + 64 u of the wave's quarter.
+    constexpr int RPL = 1024 / (DP * 2);         // rows per load
+    const int lrow = w * (KT / 4) + lane / CPR;  // + RPL * u
+    auto page_of = [&](int j) -> int {
+        const int blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
+        return j < key_end && blk < p.table_width ? table[blk] : -1;
+    };
+    int ids[Shape::LOADS];
+    auto fetch_ids = [&](int j0) {
+#pragma unroll
+        for (int u = 0; u < Shape::LOADS; ++u) ids[u] = page_of(j0 + lrow + RPL * u);
+    };
+    auto load_tile = [&](int j0, int buf) {
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < Shape::LOADS; ++u) {
+            const int row = lrow + RPL * u, j = j0 + row;
+            const int blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
+            const bool ok = (uint32_t)ids[u] < (uint64_t)p.num_blocks;
+            bad |= !ok && j < key_end;
+            const int piece = (lane % CPR) ^ Shape::turn(row);
+            const int64_t off = ((int64_t)ids[u] * p.block_size + (j - blk * p.block_size)) * row_bytes + piece * 16;
+            const bool use = ok && (EXACT || piece * 8 < dim);
+            const uint8_t* zero = reinterpret_cast<const uint8_t*>(&kZeroPiece);
+            const uint32_t dst = lds0 + buf * 2 * TILE + (w * Shape::LOADS + u) * 1024;
+            load_to_lds(dst, use ? kbase + off : zero);
+            load_to_lds(dst + TILE, use ? vbase + off : zero);
+        }
+        if (bad) gap = 1;
+    };
+
+    f32x16 acc[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+    float m = -INFINITY, l = 0.f;                // m: the scale in use, in the scores' units before c
+
+    if (threadIdx.x == 0) gap = 0;
+    __syncthreads();
+    if (ntiles > 0) {
+        fetch_ids(key_begin);
+        load_tile(key_begin, 0);
+        fetch_ids(key_begin + KT);
+    }
+    for (int t = 0; t < ntiles; ++t) {
+        const int j0 = key_begin + t * KT, buf = t & 1;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (t + 1 < ntiles) {
+            load_tile(j0 + KT, buf ^ 1);
+            fetch_ids(j0 + 2 * KT);
+        }
+        const uint8_t* kt = lds + buf * 2 * TILE;
+        const uint8_t* vt = kt + TILE;
+        if (j0 >= max(p_wave_last + 1, pre)) continue;       // nothing of the tile is seen by the wave's rows
+        f32x16 s[KB];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < QS; ++k) {
+                const int row = b * 32 + c32;
+                const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + row * (DP * 2) + ((2 * k + h32) ^ Shape::turn(row)) * 16);
+                s[b] = mfma32<BF16>(kf, q[k], s[b]);
             }
         }
-        if (__ballot(bad) != 0 && lane == 0) raise(p.status);
-        float top = s;
-        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-        const float m_new = fmaxf(m, top);
-        const float base = m_new == -INFINITY ? 0.f : m_new;     // nothing seen yet: every weight is exp(-inf)
-        const float keep = __builtin_amdgcn_exp2f((m - base) * kLog2e);
-        const float e = at >= 0 ? __builtin_amdgcn_exp2f((s - base) * kLog2e) : 0.f;
-        float sum = e;
-        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-        l = l * keep + sum;
-        m = m_new;
-        ps[w][lane] = e;
-        rows[w][lane] = at;
-        __builtin_amdgcn_wave_barrier();
-        for (int c = 0; c < 4; ++c) acc[c] *= keep;
-        const int cnt = min(64, end - j0);
-        for (int k = 0; k < cnt; ++k) {
-            if (rows[w][k] < 0) continue;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.vc + rows[w][k]);
-            const float wgt = ps[w][k];
-            for (int c = 0; c < 4; ++c)
-                if (c * 64 + lane < p.dim) acc[c] = fmaf(wgt, from_bits16(v[c * 64 + lane], p.bf16), acc[c]);
+        if constexpr (FEAT) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float v = s[b][e] * p.scale;
+                    if (p.cap > 0.f) v = p.cap * tanh_f32(v / p.cap);
+                    v *= kLog2e;
+                    if (p.slopes != nullptr)
+                        v -= slope * fabsf((float)(pos - (j0 + b * 32 + 8 * (e >> 2) + 4 * h32 + (e & 3))));
+                    s[b][e] = v;
+                }
         }
-        __builtin_amdgcn_wave_barrier();
+        const bool gaps = *(volatile int*)&gap != 0;
+        const bool clear = !gaps && j0 + KT <= max(p_wave + 1, pre) && (p.window == 0 || j0 > p_wave_last - p.window);
+        uint32_t sees[KB];
+        bool odd = false;
+        if (!clear) {
+            uint64_t pages = ~0ull;
+            if (gaps) {
+                const int id = page_of(j0 + lane);
+                pages = __ballot((uint32_t)id < (uint64_t)p.num_blocks);
+            }
+            const int hi = max(pos + 1, pre) - j0, lo = p.window > 0 ? pos - p.window + 1 - j0 : 0;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                sees[b] = ((uint32_t)(pages >> (32 * b)) & below(hi - 32 * b) & ~below(lo - 32 * b)) >> (4 * h32);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[b][e] = (sees[b] >> (8 * (e >> 2) + (e & 3)) & 1) ? s[b][e] : -INFINITY;
+            }
+            uint32_t found = 0;
+            for (int o = lane * 16; o < TILE; o += 1024) found |= odd_bits<BF16>(*reinterpret_cast<const u32x4*>(vt + o));
+            odd = __ballot(found != 0) != 0;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+        top = max_across32(top);
+        if (__ballot(top * c > m * c + 8.f || m == -INFINITY) != 0) {
+            const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
+            const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - base) * c);
+            m = m_new;
+            l *= keep;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) acc[d] *= keep;
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        u32x4 pr[2 * KB];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f32x8 pe;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    pe[e] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * half + e], c, -mc));
+                    l += pe[e];
+                }
+                pr[2 * b + half] = round8<BF16>(pe);
+            }
+        // V^T: among each 16 lanes, four keys by 16 columns per read
+        auto v_frag = [&](int k, int d) -> u32x4 {
+            uint2 part[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int row = 16 * k + 8 * y + 4 * h32 + ((lane & 15) >> 2);
+                const int piece = 4 * d + ((lane >> 4 & 1) << 1) + ((lane & 3) >> 1);
+                part[y] = read_transposed(vt + row * (DP * 2) + (piece ^ Shape::turn(row)) * 16 + (lane & 1) * 8);
+            }
+            return u32x4{part[0].x, part[0].y, part[1].x, part[1].y};
+        };
+        if (!odd) {
+#pragma unroll
+            for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+                for (int d = 0; d < DB; ++d) acc[d] = mfma32<BF16>(v_frag(k, d), pr[k], acc[d]);
+        } else {
+            // A masked tile with infinities or NaN in V: 0 times them would reach
+            // rows that do not see their key.  One key at a time, each added
+            // only to the rows that see it.
+#pragma unroll
+            for (int k = 0; k < 2 * KB; ++k)
+                for (int key = 0; key < 16; ++key) {
+                    // the key's place in the operand: half-wave (key >> 2) & 1, element
+                    const int e = (key & 3) + ((key >> 3) << 2);
+                    const bool mine = (key >> 2 & 1) == h32;
+                    const uint32_t word = (e & 1) ? 0xffff0000u : 0xffffu;
+                    const u32x4 only = {mine && (e >> 1) == 0 ? word : 0u, mine && (e >> 1) == 1 ? word : 0u,
+                                        mine && (e >> 1) == 2 ? word : 0u, mine && (e >> 1) == 3 ? word : 0u};
+                    const int bit = 16 * (k & 1) + 8 * (key >> 3) + (key & 3);
+                    const bool see = __shfl((int)sees[k >> 1], (key >> 2 & 1) * 32 + c32) >> bit & 1;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        f32x16 add;
+#pragma unroll
+                        for (int z = 0; z < 16; ++z) add[z] = 0.f;
+                        add = mfma32<BF16>(v_frag(k, d) & only, pr[k], add);
+#pragma unroll
+                        for (int z = 0; z < 16; ++z) acc[d][z] = see ? acc[d][z] + add[z] : acc[d][z];
+                    }
+                }
+        }
     }
-    uint16_t* o = reinterpret_cast<uint16_t*>(p.out + (int64_t)t * p.out_stride) + (int64_t)h * p.dim;
+    l = sum_across32(l);
+    if (threadIdx.x == 0 && gap != 0) raise(p.status);
+    __syncthreads();                             // the tiles are done with; LDS takes the output rows
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int c = 0; c < 4; ++c)
-        if (c * 64 + lane < p.dim) o[c * 64 + lane] = to_bits16(l == 0.f ? 0.f : acc[c] * inv, p.bf16);
+    uint8_t* mine = lds + w * 32 * DP * 2;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            uint32_t two[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+                two[z] = (uint32_t)to_bits16(l == 0.f ? 0.f : acc[d][4 * y + 2 * z] * inv, BF16) |
+                         (uint32_t)to_bits16(l == 0.f ? 0.f : acc[d][4 * y + 2 * z + 1] * inv, BF16) << 16;
+            *reinterpret_cast<uint2*>(mine + c32 * (DP * 2) + ((4 * d + y) ^ (c32 & 7)) * 16 + h32 * 8) = make_uint2(two[0], two[1]);
+        }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int u = 0; u < DP / 16; ++u) {
+        const int row = u * (64 / CPR) + lane / CPR, piece = lane % CPR, rr = row0 + w * 32 + row;
+        if (rr < rows && (EXACT || piece * 8 < dim)) {
+            const int tk = rr / G;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * (DP * 2) + (piece ^ (row & 7)) * 16);
+            *reinterpret_cast<u32x4*>(p.out + (int64_t)(sp.first + tk) * p.out_stride +
+                                      ((int64_t)(kvh * G + rr - tk * G) * dim + piece * 8) * 2) = v;
+        }
+    }
 }
 
 namespace {
@@ -616,8 +862,10 @@ Plan plan_of(const AttnParams& p) {
     const int64_t groups = std::max<int64_t>(1, (int64_t)p.num_reqs * p.kv_heads);
     const int64_t want = std::max<int64_t>(1, kTargetGroups / groups);
     r.min_len = (int)std::max<int64_t>(kMinSplitLen, ((keys + want - 1) / want + 31) / 32 * 32);
+    // at least 1024-key pieces are cut even where the groups are many: requests of
+    // unlike lengths then end together
     r.min_len = std::min(r.min_len, 1024);
-    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>((keys + r.min_len - 1) / r.min_len, 256));
+    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>((keys + r.min_len - 1) / r.min_len, std::min<int64_t>(std::max<int64_t>(want, 16), 256)));
     return r;
 }
 
@@ -638,6 +886,17 @@ void launch_rows(const AttnParams& p, const Plan& r, Partial part, hipStream_t s
         hipLaunchKernelGGL((join_rows_kernel<DP>), dim3(p.num_reqs, p.kv_heads * r.max_rows), dim3(256), 0, s, p, part, r.row_limit, r.max_rows, r.splits, r.min_len);
 }
 
+template <int DP, bool BF16, bool EXACT>
+void launch_chunks(const AttnParams& p, const Plan& r, hipStream_t s) {
+    const int64_t tiles = (int64_t)p.num_tokens * (p.heads / p.kv_heads) / kRowTile + p.num_reqs;
+    const dim3 grid((uint32_t)(tiles * p.kv_heads));
+    // caps, biases and a scale of zero need the whole score before the mask
+    if (p.cap > 0.f || p.slopes != nullptr || p.scale == 0.f)
+        hipLaunchKernelGGL((attention_chunk_kernel<DP, BF16, EXACT, true>), grid, dim3(256), 0, s, p, r.row_limit);
+    else
+        hipLaunchKernelGGL((attention_chunk_kernel<DP, BF16, EXACT, false>), grid, dim3(256), 0, s, p, r.row_limit);
+}
+
 }  // namespace
 
 size_t attention_workspace(const AttnParams& p) {
@@ -650,22 +909,23 @@ hipError_t launch_attention(const AttnParams& p, void* workspace, hipStream_t s)
     Partial part{};
     part.o = static_cast<float*>(workspace);
     part.ml = reinterpret_cast<float2*>(part.o + partial_rows(p, r) * r.dp);
-    if (r.nb > 0) {
-        auto go = [&](auto dp, auto bf16) {
-            constexpr int DP = decltype(dp)::value;
-            constexpr bool BF = decltype(bf16)::value;
-            if (p.dim == DP) launch_rows<DP, BF, true>(p, r, part, s);
-            else launch_rows<DP, BF, false>(p, r, part, s);
-        };
-        auto by_dim = [&](auto bf16) {
-            if (r.dp == 64) go(std::integral_constant<int, 64>{}, bf16);
-            else if (r.dp == 128) go(std::integral_constant<int, 128>{}, bf16);
-            else go(std::integral_constant<int, 256>{}, bf16);
-        };
-        if (p.bf16) by_dim(std::true_type{}); else by_dim(std::false_type{});
-    }
-    if (r.chunks)
-        hipLaunchKernelGGL(attention_any_kernel, dim3(p.num_tokens, (p.heads + 3) / 4), dim3(256), 0, s, p, r.row_limit);
+    auto go = [&](auto dp, auto bf16) {
+        constexpr int DP = decltype(dp)::value;
+        constexpr bool BF = decltype(bf16)::value;
+        if (p.dim == DP) {
+            if (r.nb > 0) launch_rows<DP, BF, true>(p, r, part, s);
+            if (r.chunks) launch_chunks<DP, BF, true>(p, r, s);
+        } else {
+            if (r.nb > 0) launch_rows<DP, BF, false>(p, r, part, s);
+            if (r.chunks) launch_chunks<DP, BF, false>(p, r, s);
+        }
+    };
+    auto by_dim = [&](auto bf16) {
+        if (r.dp == 64) go(std::integral_constant<int, 64>{}, bf16);
+        else if (r.dp == 128) go(std::integral_constant<int, 128>{}, bf16);
+        else go(std::integral_constant<int, 256>{}, bf16);
+    };
+    if (p.bf16) by_dim(std::true_type{}); else by_dim(std::false_type{});
     return hipGetLastError();
 }
 

@@ -28,7 +28,7 @@ int check_attention(const ric_attention* a, int32_t num_reqs, int32_t num_tokens
     if (a->dtype != RIC_F16 && a->dtype != RIC_BF16) return fail(RIC_EINVAL, "dtype %d is not RIC_F16 or RIC_BF16", a->dtype);
     if (a->num_heads < 1 || a->num_kv_heads < 1 || a->num_heads % a->num_kv_heads != 0)
         return fail(RIC_EINVAL, "num_heads %d is not a positive multiple of num_kv_heads %d", a->num_heads, a->num_kv_heads);
-    if (a->num_heads > 65535) return fail(RIC_EINVAL, "num_heads %d above 65535", a->num_heads);
+    if (a->num_heads > 512) return fail(RIC_EINVAL, "num_heads %d above 512", a->num_heads);
     if (a->head_dim < 8 || a->head_dim > 256 || a->head_dim % 8 != 0)
         return fail(RIC_EINVAL, "head_dim %d is not a multiple of 8 in [8, 256]", a->head_dim);
     if (a->block_size < 1) return fail(RIC_EINVAL, "block_size %d < 1", a->block_size);
@@ -36,8 +36,12 @@ int check_attention(const ric_attention* a, int32_t num_reqs, int32_t num_tokens
     if (!(a->softcap >= 0.f) || !std::isfinite(a->softcap)) return fail(RIC_EINVAL, "softcap must be finite and >= 0");
     if (a->window < 0) return fail(RIC_EINVAL, "window %d < 0", a->window);
     if (num_reqs < 0 || num_tokens < 0) return fail(RIC_EINVAL, "negative count");
-    if (num_tokens > kMaxOperatorRows || num_reqs > kMaxOperatorRows)
-        return fail(RIC_EINVAL, "num_tokens %d or num_reqs %d above %d per call", num_tokens, num_reqs, kMaxOperatorRows);
+    if (num_tokens > kMaxOperatorRows) return fail(RIC_EINVAL, "num_tokens %d above %d per call", num_tokens, kMaxOperatorRows);
+    // Grids stay below 2^24 workgroups of 256 lanes: a request's keys are cut into
+    // at most 256 pieces, its rows into tiles of 128.
+    const int64_t tiles = ((int64_t)num_tokens * (a->num_heads / a->num_kv_heads) / 128 + num_reqs) * a->num_kv_heads;
+    if (num_reqs > 65535 || tiles >= kMaxRowsPerLaunch)
+        return fail(RIC_EINVAL, "%d requests with %d tokens of %d heads are too many for one call", num_reqs, num_tokens, a->num_heads);
     if (max_query_len < 0 || max_seq_len < 0) return fail(RIC_EINVAL, "negative length");
     *p = AttnParams{};
     p->slopes = a->alibi_slopes;
