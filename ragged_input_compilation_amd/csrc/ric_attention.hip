@@ -163,6 +163,16 @@ struct Partial {
     float2* ml;      // [row][split]
 };
 
+// How a call's work is cut (see plan_of).
+struct Cut {
+    int row_limit;   // largest request of the few-rows part, in rows per K/V head
+    int max_rows;    // rows its partial results are laid out for
+    int splits;      // most pieces of a request's keys
+    int min_len;     // fewest keys per piece
+    int row_groups;  // workgroups of the few-rows part
+    int tile_groups; // workgroups of the many-rows part
+};
+
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -184,16 +194,21 @@ struct Partial {
 // P is rounded to the inputs' 8 or 11 bits (the matrix operand's type); its sum
 // is taken before the rounding, in float32.
 // ---------------------------------------------------------------------------
+template <int DP>
+constexpr int kRowsWaveLds = (kKeyTile * DP * 2 > 16 * (DP + 4) * 4) ? kKeyTile * DP * 2 : 16 * (DP + 4) * 4;
+template <int DP, int NB>
+constexpr int kRowsLds = 4 * kRowsWaveLds<DP> + 4 * 16 * NB * 8;      // bytes of LDS
+
 template <int DP, int NB, bool BF16, bool EXACT>
-__global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Partial part, int row_limit, int max_rows,
-                                                             int max_splits, int min_len) {
+__device__ __forceinline__ void rows_group(const AttnParams& p, const Partial& part, const Cut& cut, int group, uint8_t* lds) {
     constexpr int DC = DP / 32;                  // matrix steps along the head
     constexpr int CPR = DP / 8;                  // 16-byte pieces per row
-    constexpr int WAVE_LDS = (kKeyTile * DP * 2 > 16 * (DP + 4) * 4) ? kKeyTile * DP * 2 : 16 * (DP + 4) * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * WAVE_LDS];
-    __shared__ float2 stats[4][16 * NB];
+    constexpr int WAVE_LDS = kRowsWaveLds<DP>;
+    auto stats = reinterpret_cast<float2 (*)[16 * NB]>(lds + 4 * WAVE_LDS);
+    const int row_limit = cut.row_limit, max_rows = cut.max_rows, max_splits = cut.splits, min_len = cut.min_len;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c16 = lane & 15;
-    const int i = blockIdx.x / max_splits, split = blockIdx.x - i * max_splits, kvh = blockIdx.y;
+    const int kvh = group % p.kv_heads, piece_of = group / p.kv_heads;
+    const int i = piece_of / max_splits, split = piece_of - i * max_splits;
     const int G = p.heads / p.kv_heads;
     const Span sp = span_of(p, i, max_splits, min_len, kKeyTile);
     if (sp.n == 0 || split >= sp.splits) return;
@@ -471,11 +486,17 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Parti
     }
 }
 
+template <int DP, int NB, bool BF16, bool EXACT>
+__global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Partial part, Cut cut) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kRowsLds<DP, NB>];
+    rows_group<DP, NB, BF16, EXACT>(p, part, cut, blockIdx.x, lds);
+}
+
 // Joins the splits of one row: one workgroup per (request, row of a K/V head),
 // DP / 4 threads per split, the splits in a fixed order.
 template <int DP>
-__global__ __launch_bounds__(256) void join_rows_kernel(AttnParams p, Partial part, int row_limit, int max_rows,
-                                                        int max_splits, int min_len) {
+__global__ __launch_bounds__(256) void join_rows_kernel(AttnParams p, Partial part, Cut cut) {
+    const int row_limit = cut.row_limit, max_rows = cut.max_rows, max_splits = cut.splits, min_len = cut.min_len;
     constexpr int T = DP / 4, S = 256 / T;       // threads per split, splits at a time
     __shared__ f32x4 sums[S][T];
     __shared__ float lsum[S];
@@ -543,6 +564,7 @@ struct ChunkShape {
     static constexpr int CPR = DP / 8;                     // 16-byte pieces per row
     static constexpr int TILE = KT * DP * 2;               // bytes of one K or V tile
     static constexpr int LOADS = TILE / (4 * 1024);        // loads of 1 KiB per wave
+    static constexpr int LDS = 4 * TILE + 16;
     // Where piece c of row r lies in its row.  A transposed read takes four
     // neighbouring pieces of eight neighbouring rows, a K read one or two pieces
     // of 32: both spread over all 256 bytes of banks.
@@ -563,17 +585,19 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const uint8_t* src) {
 }
 
 template <int DP, bool BF16, bool EXACT, bool FEAT>
-__global__ __launch_bounds__(256, 2) void attention_chunk_kernel(AttnParams p, int row_limit) {
+__device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut, int group, uint8_t* lds) {
     using Shape = ChunkShape<DP>;
     constexpr int KT = Shape::KT, KB = Shape::KB, CPR = Shape::CPR, TILE = Shape::TILE;
     constexpr int QS = DP / 16, DB = DP / 32;
-    // [2][K, V] tiles from offset 0 (a load to LDS reaches 64 KiB), then a flag: a
-    // page that names nothing was met
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + 16];
+    // [2][K, V] tiles from LDS offset 0 (a load to LDS reaches 64 KiB), then a flag:
+    // a page that names nothing was met
     int& gap = *reinterpret_cast<int*>(lds + 4 * TILE);
+    const int row_limit = cut.row_limit;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, h32 = lane >> 5, c32 = lane & 31;
-    const int kvh = blockIdx.x % p.kv_heads;
-    const int x = gridDim.x / p.kv_heads - 1 - blockIdx.x / p.kv_heads;
+    // neighbouring workgroups (which go to different XCDs) take different K/V
+    // heads; the last tiles, with the most keys, go first
+    const int kvh = group % p.kv_heads;
+    const int x = cut.tile_groups / p.kv_heads - 1 - group / p.kv_heads;
     const int G = p.heads / p.kv_heads;
     auto start = [&](int i) { return (int)((int64_t)p.qsl[i] * G / kRowTile) + i; };
     int i = 0;
@@ -826,16 +850,37 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(AttnParams p, i
     }
 }
 
+template <int DP, bool BF16, bool EXACT, bool FEAT>
+__global__ __launch_bounds__(256, 2) void attention_chunk_kernel(AttnParams p, Cut cut) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[ChunkShape<DP>::LDS];
+    chunk_group<DP, BF16, EXACT, FEAT>(p, cut, blockIdx.x, lds);
+}
+
+// Steps of both kinds in one launch: workgroups that wait for memory and
+// workgroups that wait for the matrix units share each CU.  Blocks of eight
+// neighbours (one per XCD) are all of one kind, the kinds spread evenly.
+template <int DP, bool BF16, bool EXACT, bool FEAT>
+__global__ __launch_bounds__(256, 2) void attention_mixed_kernel(AttnParams p, Partial part, Cut cut) {
+    constexpr int LDS = ChunkShape<DP>::LDS > kRowsLds<DP, 1> ? ChunkShape<DP>::LDS : kRowsLds<DP, 1>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
+    const int64_t b = blockIdx.x >> 3, tiles = (cut.tile_groups + 7) >> 3, all = tiles + ((cut.row_groups + 7) >> 3);
+    const int before = (int)(b * tiles / all), after = (int)((b + 1) * tiles / all);
+    if (after > before) {
+        const int group = before * 8 + (blockIdx.x & 7);
+        if (group < cut.tile_groups) chunk_group<DP, BF16, EXACT, FEAT>(p, cut, group, lds);
+    } else {
+        const int group = ((int)b - before) * 8 + (blockIdx.x & 7);
+        if (group < cut.row_groups) rows_group<DP, 1, BF16, EXACT>(p, part, cut, group, lds);
+    }
+}
+
 namespace {
 
 // How a call is cut: by what the host knows, and for every length that the
 // device may hold.
 struct Plan {
-    int nb;              // 16-row blocks of the few-rows kernel, 0: not launched
-    int row_limit;       // its largest request, in rows per K/V head
-    int max_rows;        // rows its partial results are laid out for
-    int splits;          // most pieces of a request's keys
-    int min_len;         // fewest keys per piece
+    Cut cut;
+    int nb;              // 16-row blocks of the few-rows part, 0: no such part
     bool chunks;         // some request may be larger
     int dp;              // head size of the kernels
 };
@@ -848,53 +893,48 @@ Plan plan_of(const AttnParams& p) {
     const int G = p.heads / p.kv_heads;
     const int64_t most = (int64_t)p.max_q * G;
     r.dp = p.dim <= 64 ? 64 : p.dim <= 128 ? 128 : 256;
-    if (most <= 64) {
-        r.nb = most <= 16 ? 1 : most <= 32 ? 2 : 4;
-    } else if (G <= 64) {
-        r.nb = G <= 16 ? 1 : G <= 32 ? 2 : 4;
-        r.chunks = true;
-    } else {
-        r.chunks = true;
-    }
-    r.row_limit = 16 * r.nb;
-    r.max_rows = (int)std::min<int64_t>(most, r.row_limit);
+    // Requests of up to 64 rows per K/V head take the few-rows kernel; beside
+    // larger ones, those of a single token do.
+    const int64_t few = most <= 64 ? most : G <= 64 ? G : 0;
+    r.chunks = most > 64;
+    r.nb = few == 0 ? 0 : few <= 16 ? 1 : few <= 32 ? 2 : 4;
+    Cut& c = r.cut;
+    c.row_limit = 16 * r.nb;
+    c.max_rows = (int)std::min<int64_t>(most, c.row_limit);
     const int64_t keys = p.window > 0 && p.prefix == nullptr ? std::min<int64_t>(p.max_seq, (int64_t)p.window + p.max_q + 31) : p.max_seq;
     const int64_t groups = std::max<int64_t>(1, (int64_t)p.num_reqs * p.kv_heads);
     const int64_t want = std::max<int64_t>(1, kTargetGroups / groups);
-    r.min_len = (int)std::max<int64_t>(kMinSplitLen, ((keys + want - 1) / want + 31) / 32 * 32);
     // at least 1024-key pieces are cut even where the groups are many: requests of
     // unlike lengths then end together
-    r.min_len = std::min(r.min_len, 1024);
-    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>((keys + r.min_len - 1) / r.min_len, std::min<int64_t>(std::max<int64_t>(want, 16), 256)));
+    c.min_len = (int)std::min<int64_t>(1024, std::max<int64_t>(kMinSplitLen, ((keys + want - 1) / want + 31) / 32 * 32));
+    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>((keys + c.min_len - 1) / c.min_len, std::min<int64_t>(std::max<int64_t>(want, 16), 256)));
+    c.row_groups = r.nb > 0 ? p.num_reqs * c.splits * p.kv_heads : 0;
+    c.tile_groups = r.chunks ? (int)(((int64_t)p.num_tokens * G / kRowTile + p.num_reqs) * p.kv_heads) : 0;
     return r;
 }
 
 int64_t partial_rows(const AttnParams& p, const Plan& r) {
-    return r.splits > 1 ? (int64_t)p.num_reqs * p.kv_heads * r.max_rows * r.splits : 0;
+    return r.nb > 0 && r.cut.splits > 1 ? (int64_t)p.num_reqs * p.kv_heads * r.cut.max_rows * r.cut.splits : 0;
 }
 
 template <int DP, bool BF16, bool EXACT>
-void launch_rows(const AttnParams& p, const Plan& r, Partial part, hipStream_t s) {
-    const dim3 grid((uint32_t)(p.num_reqs * r.splits), p.kv_heads);
-    if (r.nb == 1)
-        hipLaunchKernelGGL((attention_rows_kernel<DP, 1, BF16, EXACT>), grid, dim3(256), 0, s, p, part, r.row_limit, r.max_rows, r.splits, r.min_len);
-    else if (r.nb == 2)
-        hipLaunchKernelGGL((attention_rows_kernel<DP, 2, BF16, EXACT>), grid, dim3(256), 0, s, p, part, r.row_limit, r.max_rows, r.splits, r.min_len);
-    else
-        hipLaunchKernelGGL((attention_rows_kernel<DP, 4, BF16, EXACT>), grid, dim3(256), 0, s, p, part, r.row_limit, r.max_rows, r.splits, r.min_len);
-    if (r.splits > 1)
-        hipLaunchKernelGGL((join_rows_kernel<DP>), dim3(p.num_reqs, p.kv_heads * r.max_rows), dim3(256), 0, s, p, part, r.row_limit, r.max_rows, r.splits, r.min_len);
-}
-
-template <int DP, bool BF16, bool EXACT>
-void launch_chunks(const AttnParams& p, const Plan& r, hipStream_t s) {
-    const int64_t tiles = (int64_t)p.num_tokens * (p.heads / p.kv_heads) / kRowTile + p.num_reqs;
-    const dim3 grid((uint32_t)(tiles * p.kv_heads));
+void launch(const AttnParams& p, const Plan& r, Partial part, hipStream_t s) {
+    const Cut& c = r.cut;
     // caps, biases and a scale of zero need the whole score before the mask
-    if (p.cap > 0.f || p.slopes != nullptr || p.scale == 0.f)
-        hipLaunchKernelGGL((attention_chunk_kernel<DP, BF16, EXACT, true>), grid, dim3(256), 0, s, p, r.row_limit);
-    else
-        hipLaunchKernelGGL((attention_chunk_kernel<DP, BF16, EXACT, false>), grid, dim3(256), 0, s, p, r.row_limit);
+    const bool feat = p.cap > 0.f || p.slopes != nullptr || p.scale == 0.f;
+    if (r.chunks && r.nb == 1) {
+        const dim3 grid(((c.tile_groups + 7) / 8 + (c.row_groups + 7) / 8) * 8);
+        if (feat) hipLaunchKernelGGL((attention_mixed_kernel<DP, BF16, EXACT, true>), grid, dim3(256), 0, s, p, part, c);
+        else hipLaunchKernelGGL((attention_mixed_kernel<DP, BF16, EXACT, false>), grid, dim3(256), 0, s, p, part, c);
+    } else {
+        if (r.nb == 1) hipLaunchKernelGGL((attention_rows_kernel<DP, 1, BF16, EXACT>), dim3(c.row_groups), dim3(256), 0, s, p, part, c);
+        if (r.nb == 2) hipLaunchKernelGGL((attention_rows_kernel<DP, 2, BF16, EXACT>), dim3(c.row_groups), dim3(256), 0, s, p, part, c);
+        if (r.nb == 4) hipLaunchKernelGGL((attention_rows_kernel<DP, 4, BF16, EXACT>), dim3(c.row_groups), dim3(256), 0, s, p, part, c);
+        if (r.chunks && feat) hipLaunchKernelGGL((attention_chunk_kernel<DP, BF16, EXACT, true>), dim3(c.tile_groups), dim3(256), 0, s, p, c);
+        if (r.chunks && !feat) hipLaunchKernelGGL((attention_chunk_kernel<DP, BF16, EXACT, false>), dim3(c.tile_groups), dim3(256), 0, s, p, c);
+    }
+    if (r.nb > 0 && c.splits > 1)
+        hipLaunchKernelGGL((join_rows_kernel<DP>), dim3(p.num_reqs, p.kv_heads * c.max_rows), dim3(256), 0, s, p, part, c);
 }
 
 }  // namespace
@@ -909,21 +949,14 @@ hipError_t launch_attention(const AttnParams& p, void* workspace, hipStream_t s)
     Partial part{};
     part.o = static_cast<float*>(workspace);
     part.ml = reinterpret_cast<float2*>(part.o + partial_rows(p, r) * r.dp);
-    auto go = [&](auto dp, auto bf16) {
-        constexpr int DP = decltype(dp)::value;
-        constexpr bool BF = decltype(bf16)::value;
-        if (p.dim == DP) {
-            if (r.nb > 0) launch_rows<DP, BF, true>(p, r, part, s);
-            if (r.chunks) launch_chunks<DP, BF, true>(p, r, s);
-        } else {
-            if (r.nb > 0) launch_rows<DP, BF, false>(p, r, part, s);
-            if (r.chunks) launch_chunks<DP, BF, false>(p, r, s);
-        }
+    auto with = [&](auto dp, auto bf16) {
+        if (p.dim == decltype(dp)::value) launch<decltype(dp)::value, decltype(bf16)::value, true>(p, r, part, s);
+        else launch<decltype(dp)::value, decltype(bf16)::value, false>(p, r, part, s);
     };
     auto by_dim = [&](auto bf16) {
-        if (r.dp == 64) go(std::integral_constant<int, 64>{}, bf16);
-        else if (r.dp == 128) go(std::integral_constant<int, 128>{}, bf16);
-        else go(std::integral_constant<int, 256>{}, bf16);
+        if (r.dp == 64) with(std::integral_constant<int, 64>{}, bf16);
+        else if (r.dp == 128) with(std::integral_constant<int, 128>{}, bf16);
+        else with(std::integral_constant<int, 256>{}, bf16);
     };
     if (p.bf16) by_dim(std::true_type{}); else by_dim(std::false_type{});
     return hipGetLastError();

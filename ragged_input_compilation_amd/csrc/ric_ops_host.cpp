@@ -37,10 +37,10 @@ int check_attention(const ric_attention* a, int32_t num_reqs, int32_t num_tokens
     if (a->window < 0) return fail(RIC_EINVAL, "window %d < 0", a->window);
     if (num_reqs < 0 || num_tokens < 0) return fail(RIC_EINVAL, "negative count");
     if (num_tokens > kMaxOperatorRows) return fail(RIC_EINVAL, "num_tokens %d above %d per call", num_tokens, kMaxOperatorRows);
-    // Grids stay below 2^24 workgroups of 256 lanes: a request's keys are cut into
-    // at most 256 pieces, its rows into tiles of 128.
+    // Grids stay below 2^24 workgroups of 256 lanes: a request's rows are cut into
+    // tiles of 128, its keys into 16 pieces per K/V head (256 where requests are few).
     const int64_t tiles = ((int64_t)num_tokens * (a->num_heads / a->num_kv_heads) / 128 + num_reqs) * a->num_kv_heads;
-    if (num_reqs > 65535 || tiles >= kMaxRowsPerLaunch)
+    if (num_reqs > 65535 || (int64_t)num_reqs * a->num_kv_heads >= (1 << 20) || tiles >= kMaxRowsPerLaunch)
         return fail(RIC_EINVAL, "%d requests with %d tokens of %d heads are too many for one call", num_reqs, num_tokens, a->num_heads);
     if (max_query_len < 0 || max_seq_len < 0) return fail(RIC_EINVAL, "negative length");
     *p = AttnParams{};
