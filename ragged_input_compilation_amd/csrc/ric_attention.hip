@@ -207,7 +207,7 @@ __device__ __forceinline__ void rows_group(const AttnParams& p, const Partial& p
     auto stats = reinterpret_cast<float2 (*)[16 * NB]>(lds + 4 * WAVE_LDS);
     const int row_limit = cut.row_limit, max_rows = cut.max_rows, max_splits = cut.splits, min_len = cut.min_len;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c16 = lane & 15;
-    const int kvh = group % p.kv_heads, piece_of = group / p.kv_heads;
+    const int pieces = p.num_reqs * max_splits, kvh = group / pieces, piece_of = group - kvh * pieces;
     const int i = piece_of / max_splits, split = piece_of - i * max_splits;
     const int G = p.heads / p.kv_heads;
     const Span sp = span_of(p, i, max_splits, min_len, kKeyTile);
@@ -487,7 +487,7 @@ __device__ __forceinline__ void rows_group(const AttnParams& p, const Partial& p
 }
 
 template <int DP, int NB, bool BF16, bool EXACT>
-__global__ __launch_bounds__(256) void attention_rows_kernel(AttnParams p, Partial part, Cut cut) {
+__global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void attention_rows_kernel(AttnParams p, Partial part, Cut cut) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kRowsLds<DP, NB>];
     rows_group<DP, NB, BF16, EXACT>(p, part, cut, blockIdx.x, lds);
 }
@@ -531,6 +531,71 @@ __global__ __launch_bounds__(256) void join_rows_kernel(AttnParams p, Partial pa
     const int tok = r / G, h = kvh * G + (r - tok * G);
     uint16_t* dst = reinterpret_cast<uint16_t*>(p.out + (int64_t)(sp.first + tok) * p.out_stride) + (int64_t)h * p.dim + d4 * 4;
     for (int e = 0; e < 4; ++e) dst[e] = to_bits16(l == 0.f ? 0.f : o[e] * inv, p.bf16);
+}
+
+// One row by one wave, key by key where the weights meet V: the way out for rows
+// that stand next to infinities or NaN they do not see.  A lane scores one key of
+// a group of 64, then the wave adds the group's V rows, each lane holding up to
+// four output columns.  `scratch`: 1.75 KiB of LDS of the wave's own.
+__device__ __forceinline__ void exact_row(const AttnParams& p, const int32_t* table, int tok, int head, int kvh, int pos, int begin,
+                                       int end, uint8_t* scratch) {
+    const int lane = threadIdx.x & 63;
+    float* qs = reinterpret_cast<float*>(scratch);
+    float* ps = qs + 256;
+    int64_t* at = reinterpret_cast<int64_t*>(ps + 64);
+    const float slope = p.slopes != nullptr ? p.slopes[head] : 0.f;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q + (int64_t)tok * p.q_stride) + (int64_t)head * p.dim;
+    for (int d = lane; d < p.dim; d += 64) qs[d] = from_bits16(q[d], p.bf16);
+    const int64_t row_bytes = (int64_t)p.kv_heads * p.dim * 2;
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = begin; j0 < end; j0 += 64) {
+        const int j = j0 + lane, blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
+        const int64_t id = j < end && blk < p.table_width ? table[blk] : -1;
+        const int64_t where = id >= 0 && id < p.num_blocks
+            ? (id * p.block_size + (j - blk * p.block_size)) * row_bytes + (int64_t)kvh * p.dim * 2 : -1;
+        float s = -INFINITY;
+        if (where >= 0) {
+            float dot = 0.f;
+            for (int d = 0; d < p.dim; d += 8) {
+                const u32x4 k = *reinterpret_cast<const u32x4*>(p.kc + where + d * 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dot = fmaf(from_bits16(k[e] & 0xffffu, p.bf16), qs[d + 2 * e], dot);
+                    dot = fmaf(from_bits16(k[e] >> 16, p.bf16), qs[d + 2 * e + 1], dot);
+                }
+            }
+            s = dot * p.scale;
+            if (p.cap > 0.f) s = p.cap * tanh_f32(s / p.cap);
+            s = (s - slope * fabsf((float)(pos - j))) * kLog2e;
+        }
+        float top = s;
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
+        const float keep = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - base);
+        const float e = where >= 0 ? __builtin_amdgcn_exp2f(s - base) : 0.f;
+        float sum = e;
+        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+        l = l * keep + sum;
+        m = m_new;
+        ps[lane] = e;
+        at[lane] = where;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] *= keep;
+        for (int k = 0; k < min(64, end - j0); ++k) {
+            if (at[k] < 0) continue;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.vc + at[k]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c * 64 + lane < p.dim) acc[c] = fmaf(ps[k], from_bits16(v[c * 64 + lane], p.bf16), acc[c]);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out + (int64_t)tok * p.out_stride) + (int64_t)head * p.dim;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c * 64 + lane < p.dim) o[c * 64 + lane] = to_bits16(l == 0.f ? 0.f : acc[c] * inv, p.bf16);
 }
 
 // ---------------------------------------------------------------------------
@@ -591,7 +656,8 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
     constexpr int QS = DP / 16, DB = DP / 32;
     // [2][K, V] tiles from LDS offset 0 (a load to LDS reaches 64 KiB), then a flag:
     // a page that names nothing was met
-    int& gap = *reinterpret_cast<int*>(lds + 4 * TILE);
+    // (an LDS pointer: a flat or volatile read would wait for the loads in flight)
+    __attribute__((address_space(3))) int* gap = (__attribute__((address_space(3))) int*)(lds + 4 * TILE);
     const int row_limit = cut.row_limit;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, h32 = lane >> 5, c32 = lane & 31;
     // neighbouring workgroups (which go to different XCDs) take different K/V
@@ -648,35 +714,31 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
     const int p_wave = __builtin_amdgcn_readfirstlane(sp.seq - sp.n + min(rows - 1, row0 + w * 32) / G);
     const int p_wave_last = __builtin_amdgcn_readfirstlane(sp.seq - sp.n + min(rows - 1, row0 + w * 32 + 31) / G);
 
-    // This lane's part of the tile loads: pieces lane + 64 u of the wave's quarter.
-    constexpr int RPL = 1024 / (DP * 2);         // rows per load
-    const int lrow = w * (KT / 4) + lane / CPR;  // + RPL * u
-    auto page_of = [&](int j) -> int {
-        const int blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
-        return j < key_end && blk < p.table_width ? table[blk] : -1;
-    };
-    int ids[Shape::LOADS];
-    auto fetch_ids = [&](int j0) {
-#pragma unroll
-        for (int u = 0; u < Shape::LOADS; ++u) ids[u] = page_of(j0 + lrow + RPL * u);
-    };
-    auto load_tile = [&](int j0, int buf) {
-        bool bad = false;
+    // The wave loads a quarter of each tile: KT / 4 rows, RPL of them per load.
+    // Lane c looks up the page of row c of the quarter, one tile ahead, always (a
+    // key past the end looks up the last readable entry), so that nothing but the
+    // next tile's address computation waits for it.
+    constexpr int RPL = 1024 / (DP * 2), QROWS = KT / 4;
+    const int last_entry = max(0, min(p.table_width, (max(key_end, 1) - 1) / p.block_size + 1) - 1);
+    auto block_of = [&](int j) { return p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size; };
+    auto lookup = [&](int j0) { return table[min(block_of(j0 + w * QROWS + (lane & (QROWS - 1))), last_entry)]; };
+    auto load_tile = [&](int j0, int buf, int id) {
+        const int j = j0 + w * QROWS + (lane & (QROWS - 1)), blk = block_of(j);
+        const bool named = blk < p.table_width && (uint32_t)id < (uint64_t)p.num_blocks;
+        if (!named && j < key_end) *gap = 1;
+        const int slot = named && j < key_end ? id * p.block_size + (j - blk * p.block_size) : -1;
 #pragma unroll
         for (int u = 0; u < Shape::LOADS; ++u) {
-            const int row = lrow + RPL * u, j = j0 + row;
-            const int blk = p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size;
-            const bool ok = (uint32_t)ids[u] < (uint64_t)p.num_blocks;
-            bad |= !ok && j < key_end;
-            const int piece = (lane % CPR) ^ Shape::turn(row);
-            const int64_t off = ((int64_t)ids[u] * p.block_size + (j - blk * p.block_size)) * row_bytes + piece * 16;
-            const bool use = ok && (EXACT || piece * 8 < dim);
+            const int row = lane / CPR + RPL * u;          // of the quarter
+            const int from = __shfl(slot, row);
+            const int piece = (lane % CPR) ^ Shape::turn(w * QROWS + row);
+            const int64_t off = (int64_t)from * row_bytes + piece * 16;
+            const bool use = from >= 0 && (EXACT || piece * 8 < dim);
             const uint8_t* zero = reinterpret_cast<const uint8_t*>(&kZeroPiece);
             const uint32_t dst = lds0 + buf * 2 * TILE + (w * Shape::LOADS + u) * 1024;
             load_to_lds(dst, use ? kbase + off : zero);
             load_to_lds(dst + TILE, use ? vbase + off : zero);
         }
-        if (bad) gap = 1;
     };
 
     f32x16 acc[DB];
@@ -684,22 +746,27 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+    bool poisoned = false;
     float m = -INFINITY, l = 0.f;                // m: the scale in use, in the scores' units before c
 
-    if (threadIdx.x == 0) gap = 0;
+    if (threadIdx.x == 0) *gap = 0;
     __syncthreads();
-    if (ntiles > 0) {
-        fetch_ids(key_begin);
-        load_tile(key_begin, 0);
-        fetch_ids(key_begin + KT);
+    int next_id = 0;
+    if (ntiles > 0 && p.table_width > 0) {
+        load_tile(key_begin, 0, lookup(key_begin));
+        next_id = lookup(key_begin + KT);
+    } else if (ntiles > 0) {
+        load_tile(key_begin, 0, -1);
+        next_id = -1;
     }
     for (int t = 0; t < ntiles; ++t) {
         const int j0 = key_begin + t * KT, buf = t & 1;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
+        const bool gaps = *gap != 0;
         if (t + 1 < ntiles) {
-            load_tile(j0 + KT, buf ^ 1);
-            fetch_ids(j0 + 2 * KT);
+            load_tile(j0 + KT, buf ^ 1, next_id);
+            if (p.table_width > 0) next_id = lookup(j0 + 2 * KT);
         }
         const uint8_t* kt = lds + buf * 2 * TILE;
         const uint8_t* vt = kt + TILE;
@@ -709,12 +776,13 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
         for (int b = 0; b < KB; ++b) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
+            const int row = b * 32 + c32;
+            u32x4 kf[QS];
 #pragma unroll
-            for (int k = 0; k < QS; ++k) {
-                const int row = b * 32 + c32;
-                const u32x4 kf = *reinterpret_cast<const u32x4*>(kt + row * (DP * 2) + ((2 * k + h32) ^ Shape::turn(row)) * 16);
-                s[b] = mfma32<BF16>(kf, q[k], s[b]);
-            }
+            for (int k = 0; k < QS; ++k)
+                kf[k] = *reinterpret_cast<const u32x4*>(kt + row * (DP * 2) + ((2 * k + h32) ^ Shape::turn(row)) * 16);
+#pragma unroll
+            for (int k = 0; k < QS; ++k) s[b] = mfma32<BF16>(kf[k], q[k], s[b]);
         }
         if constexpr (FEAT) {
 #pragma unroll
@@ -729,27 +797,28 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
                     s[b][e] = v;
                 }
         }
-        const bool gaps = *(volatile int*)&gap != 0;
         const bool clear = !gaps && j0 + KT <= max(p_wave + 1, pre) && (p.window == 0 || j0 > p_wave_last - p.window);
-        uint32_t sees[KB];
-        bool odd = false;
         if (!clear) {
             uint64_t pages = ~0ull;
             if (gaps) {
-                const int id = page_of(j0 + lane);
+                const int blk = block_of(j0 + lane);
+                const int id = j0 + lane < key_end && blk < p.table_width ? table[blk] : -1;
                 pages = __ballot((uint32_t)id < (uint64_t)p.num_blocks);
             }
             const int hi = max(pos + 1, pre) - j0, lo = p.window > 0 ? pos - p.window + 1 - j0 : 0;
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
-                sees[b] = ((uint32_t)(pages >> (32 * b)) & below(hi - 32 * b) & ~below(lo - 32 * b)) >> (4 * h32);
+                const uint32_t sees = ((uint32_t)(pages >> (32 * b)) & below(hi - 32 * b) & ~below(lo - 32 * b)) >> (4 * h32);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[b][e] = (sees[b] >> (8 * (e >> 2) + (e & 3)) & 1) ? s[b][e] : -INFINITY;
+                for (int e = 0; e < 16; ++e) s[b][e] = (sees >> (8 * (e >> 2) + (e & 3)) & 1) ? s[b][e] : -INFINITY;
             }
             uint32_t found = 0;
             for (int o = lane * 16; o < TILE; o += 1024) found |= odd_bits<BF16>(*reinterpret_cast<const u32x4*>(vt + o));
-            odd = __ballot(found != 0) != 0;
+            // A masked tile with infinities or NaN in V: 0 times them would reach
+            // rows that do not see their key.  The wave's rows are done another way.
+            poisoned |= __ballot(found != 0) != 0;
         }
+        if (poisoned) continue;
         float top = s[0][0];
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -766,6 +835,9 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
         u32x4 pr[2 * KB];
+        f32x8 sum;                               // eight short chains instead of one long one
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -774,10 +846,11 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     pe[e] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * half + e], c, -mc));
-                    l += pe[e];
+                    sum[e] += pe[e];
                 }
                 pr[2 * b + half] = round8<BF16>(pe);
             }
+        l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
         // V^T: among each 16 lanes, four keys by 16 columns per read
         auto v_frag = [&](int k, int d) -> u32x4 {
             uint2 part[2];
@@ -789,41 +862,30 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
             }
             return u32x4{part[0].x, part[0].y, part[1].x, part[1].y};
         };
-        if (!odd) {
+        u32x4 vf[2][DB];                         // one step of 16 keys ahead
 #pragma unroll
-            for (int k = 0; k < 2 * KB; ++k)
+        for (int d = 0; d < DB; ++d) vf[0][d] = v_frag(0, d);
 #pragma unroll
-                for (int d = 0; d < DB; ++d) acc[d] = mfma32<BF16>(v_frag(k, d), pr[k], acc[d]);
-        } else {
-            // A masked tile with infinities or NaN in V: 0 times them would reach
-            // rows that do not see their key.  One key at a time, each added
-            // only to the rows that see it.
+        for (int k = 0; k < 2 * KB; ++k) {
+            if (k + 1 < 2 * KB) {
 #pragma unroll
-            for (int k = 0; k < 2 * KB; ++k)
-                for (int key = 0; key < 16; ++key) {
-                    // the key's place in the operand: half-wave (key >> 2) & 1, element
-                    const int e = (key & 3) + ((key >> 3) << 2);
-                    const bool mine = (key >> 2 & 1) == h32;
-                    const uint32_t word = (e & 1) ? 0xffff0000u : 0xffffu;
-                    const u32x4 only = {mine && (e >> 1) == 0 ? word : 0u, mine && (e >> 1) == 1 ? word : 0u,
-                                        mine && (e >> 1) == 2 ? word : 0u, mine && (e >> 1) == 3 ? word : 0u};
-                    const int bit = 16 * (k & 1) + 8 * (key >> 3) + (key & 3);
-                    const bool see = __shfl((int)sees[k >> 1], (key >> 2 & 1) * 32 + c32) >> bit & 1;
+                for (int d = 0; d < DB; ++d) vf[(k + 1) & 1][d] = v_frag(k + 1, d);
+            }
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        f32x16 add;
-#pragma unroll
-                        for (int z = 0; z < 16; ++z) add[z] = 0.f;
-                        add = mfma32<BF16>(v_frag(k, d) & only, pr[k], add);
-#pragma unroll
-                        for (int z = 0; z < 16; ++z) acc[d][z] = see ? acc[d][z] + add[z] : acc[d][z];
-                    }
-                }
+            for (int d = 0; d < DB; ++d) acc[d] = mfma32<BF16>(vf[k & 1][d], pr[k], acc[d]);
         }
     }
     l = sum_across32(l);
-    if (threadIdx.x == 0 && gap != 0) raise(p.status);
+    if (threadIdx.x == 0 && *gap != 0) raise(p.status);
     __syncthreads();                             // the tiles are done with; LDS takes the output rows
+    if (poisoned) {
+        for (int k = 0; k < 32 && row0 + w * 32 + k < rows; ++k) {
+            const int rr = row0 + w * 32 + k, tk = rr / G, at = sp.seq - sp.n + tk;
+            exact_row(p, table, sp.first + tk, kvh * G + rr - tk * G, kvh, at, p.window > 0 ? max(0, at + 1 - p.window) : 0,
+                      min(sp.seq, max(at + 1, pre)), lds + w * 32 * DP * 2);
+        }
+        return;
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint8_t* mine = lds + w * 32 * DP * 2;
 #pragma unroll
