@@ -86,7 +86,7 @@ __device__ __forceinline__ u32x4 round8(f32x8 x) {
 // Four 16-bit elements of one column from four consecutive rows: among each 16
 // lanes, lane t names 8 bytes of row t / 4 (columns 4 (t % 4)..+3) and receives
 // column t of the four rows.
-__device__ __forceinline__ uint2 read_transposed(const uint8_t* lds) {
+__device__ __forceinline__ uint2 read_transposed(const __attribute__((address_space(3))) uint8_t* lds) {
     typedef s16x4 __attribute__((address_space(3)))* lds_ptr;
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds)));
 }
@@ -402,7 +402,7 @@ __device__ __forceinline__ void rows_group(const AttnParams& p, const Partial& p
             uint2 half[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                half[s] = read_transposed(my + at(16 * s + 4 * g + (c16 >> 2), 2 * d + ((c16 & 3) >> 1)) + (c16 & 1) * 8);
+                half[s] = read_transposed((const __attribute__((address_space(3))) uint8_t*)my + at(16 * s + 4 * g + (c16 >> 2), 2 * d + ((c16 & 3) >> 1)) + (c16 & 1) * 8);
             const u32x4 vt = {half[0].x, half[0].y, half[1].x, half[1].y};
             if (odd_tile == 0) {
 #pragma unroll
@@ -614,12 +614,11 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const int32_t* ta
 //   K and V go from memory to LDS without registers (16 bytes per lane, the next
 //   tile while this one is computed); the lanes of a load pick which piece of
 //   which row they fetch, which turns rows against each other (no bank is hit
-//   more often than the access needs) and sends keys without a page to a zero.
+//   more often than the access needs).  A key past the end fetches the last one,
+//   a key without a page the cache's first row; both are masked.
 //   The maximum a row is scaled by is only raised when a new one exceeds it by
 //   more than 2^8, so most tiles leave the 64 accumulators untouched.
 // ---------------------------------------------------------------------------
-__device__ const u32x4 kZeroPiece = {0, 0, 0, 0};
-
 constexpr int kRowTile = 128;
 
 template <int DP>
@@ -639,14 +638,37 @@ struct ChunkShape {
     }
 };
 
-// Copies 16 bytes per lane from memory to LDS at `lds` + 16 * lane.  Complete
-// after s_waitcnt vmcnt(0).  Written as text because the compiler, given its own
-// form, waits for the load in flight before every read of the other tile.  It
-// writes no register; M0, which holds the LDS address, is left as it was.
+// Copies 16 bytes per lane from memory (base + offset) to LDS at `lds` + 16 * lane.
+// Complete after s_waitcnt vmcnt(0).  Written as text because the compiler, given
+// its own form, waits for the load in flight before every read of the other
+// tile.  It writes no vector register; M0, which holds the LDS address, is left
+// as it was.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const uint8_t* base, uint32_t offset) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base) : "memory");
+}
+// The same from any 64-bit address.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, const uint8_t* src) {
     uint32_t m0;
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+}
+
+// Eight values' sum added to `sum`, from the rounded pairs.
+template <bool BF16>
+__device__ __forceinline__ float add_pairs(u32x4 x, float sum) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t two = x[k];
+        if constexpr (BF16)
+            sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), bf16x2{(__bf16)1.f, (__bf16)1.f}, sum, false);
+        else
+            sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, two), f16x2{(_Float16)1.f, (_Float16)1.f}, sum, false);
+    }
+    return sum;
 }
 
 template <int DP, bool BF16, bool EXACT, bool FEAT>
@@ -715,31 +737,57 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
     const int p_wave_last = __builtin_amdgcn_readfirstlane(sp.seq - sp.n + min(rows - 1, row0 + w * 32 + 31) / G);
 
     // The wave loads a quarter of each tile: KT / 4 rows, RPL of them per load.
-    // Lane c looks up the page of row c of the quarter, one tile ahead, always (a
-    // key past the end looks up the last readable entry), so that nothing but the
-    // next tile's address computation waits for it.
+    // Lane c looks up the page of row c of the quarter, one tile ahead, so that
+    // nothing but the next tile's address computation waits for it.
     constexpr int RPL = 1024 / (DP * 2), QROWS = KT / 4;
-    const int last_entry = max(0, min(p.table_width, (max(key_end, 1) - 1) / p.block_size + 1) - 1);
     auto block_of = [&](int j) { return p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size; };
-    auto lookup = [&](int j0) { return table[min(block_of(j0 + w * QROWS + (lane & (QROWS - 1))), last_entry)]; };
-    auto load_tile = [&](int j0, int buf, int id) {
-        const int j = j0 + w * QROWS + (lane & (QROWS - 1)), blk = block_of(j);
-        const bool named = blk < p.table_width && (uint32_t)id < (uint64_t)p.num_blocks;
-        if (!named && j < key_end) *gap = 1;
-        const int slot = named && j < key_end ? id * p.block_size + (j - blk * p.block_size) : -1;
+    auto key_of = [&](int j0) { return min(j0 + w * QROWS + (lane & (QROWS - 1)), key_end - 1); };
+    auto lookup = [&](int j0) { return table[min(block_of(key_of(j0)), p.table_width - 1)]; };
+    int piece_off[Shape::LOADS];                 // where in a row the lane's piece of load u starts
 #pragma unroll
-        for (int u = 0; u < Shape::LOADS; ++u) {
-            const int row = lane / CPR + RPL * u;          // of the quarter
-            const int from = __shfl(slot, row);
-            const int piece = (lane % CPR) ^ Shape::turn(w * QROWS + row);
-            const int64_t off = (int64_t)from * row_bytes + piece * 16;
-            const bool use = from >= 0 && (EXACT || piece * 8 < dim);
-            const uint8_t* zero = reinterpret_cast<const uint8_t*>(&kZeroPiece);
-            const uint32_t dst = lds0 + buf * 2 * TILE + (w * Shape::LOADS + u) * 1024;
-            load_to_lds(dst, use ? kbase + off : zero);
-            load_to_lds(dst + TILE, use ? vbase + off : zero);
+    for (int u = 0; u < Shape::LOADS; ++u) {
+        const int piece = (lane % CPR) ^ Shape::turn(w * QROWS + lane / CPR + RPL * u);
+        piece_off[u] = EXACT || piece * 8 < dim ? piece * 16 : 0;
+    }
+    const bool near = p.num_blocks * p.block_size * row_bytes < (int64_t(1) << 32);
+    auto load_tile = [&](int j0, int buf, int id) {
+        const int j = key_of(j0), blk = block_of(j);
+        const bool named = blk < p.table_width && (uint32_t)id < (uint64_t)p.num_blocks;
+        if (!named) *gap = 1;
+        const uint32_t slot = named ? id * p.block_size + (j - blk * p.block_size) : 0;
+        const uint32_t dst = lds0 + buf * 2 * TILE + w * Shape::LOADS * 1024;
+        if (near) {
+            const uint32_t start_of = slot * (uint32_t)row_bytes;
+#pragma unroll
+            for (int u = 0; u < Shape::LOADS; ++u) {
+                const uint32_t off = __shfl(start_of, lane / CPR + RPL * u) + piece_off[u];
+                load_to_lds(dst + u * 1024, kbase, off);
+                load_to_lds(dst + u * 1024 + TILE, vbase, off);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < Shape::LOADS; ++u) {
+                const int64_t off = (int64_t)__shfl(slot, lane / CPR + RPL * u) * row_bytes + piece_off[u];
+                load_to_lds(dst + u * 1024, kbase + off);
+                load_to_lds(dst + u * 1024 + TILE, vbase + off);
+            }
         }
     };
+    // Where the lane's operands lie in a tile: K row c32 (+ 32 b), step k (+ 8); V^T
+    // rows of its half and quarter (+ 16 k), columns d (+ 4).  Everything else
+    // about an address is a constant of the unrolled loop.
+    typedef const __attribute__((address_space(3))) uint8_t* lds_ptr;
+    constexpr int KA = QS < 8 ? QS : 8, VA = DB < 4 ? DB : 4;
+    lds_ptr ka[KA], va[2][VA];
+#pragma unroll
+    for (int k = 0; k < KA; ++k) ka[k] = (lds_ptr)lds + c32 * (DP * 2) + ((2 * k + h32) ^ Shape::turn(c32)) * 16;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int d = 0; d < VA; ++d) {
+            const int row = 8 * y + 4 * h32 + ((lane & 15) >> 2), piece = 4 * d + ((lane >> 4 & 1) << 1) + ((lane & 3) >> 1);
+            va[y][d] = (lds_ptr)lds + row * (DP * 2) + (piece ^ Shape::turn(row)) * 16 + (lane & 1) * 8;
+        }
 
     f32x16 acc[DB];
 #pragma unroll
@@ -751,38 +799,33 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
 
     if (threadIdx.x == 0) *gap = 0;
     __syncthreads();
-    int next_id = 0;
-    if (ntiles > 0 && p.table_width > 0) {
-        load_tile(key_begin, 0, lookup(key_begin));
-        next_id = lookup(key_begin + KT);
-    } else if (ntiles > 0) {
-        load_tile(key_begin, 0, -1);
-        next_id = -1;
+    int next_id = -1;
+    if (ntiles > 0) {
+        load_tile(key_begin, 0, p.table_width > 0 ? lookup(key_begin) : -1);
+        if (p.table_width > 0) next_id = lookup(key_begin + KT);
     }
-    for (int t = 0; t < ntiles; ++t) {
-        const int j0 = key_begin + t * KT, buf = t & 1;
+    auto step = [&](auto which, int t) __attribute__((always_inline)) {
+        constexpr int BUF = decltype(which)::value, K0 = BUF * 2 * TILE, V0 = K0 + TILE;
+        const int j0 = key_begin + t * KT;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         const bool gaps = *gap != 0;
         if (t + 1 < ntiles) {
-            load_tile(j0 + KT, buf ^ 1, next_id);
+            load_tile(j0 + KT, BUF ^ 1, next_id);
             if (p.table_width > 0) next_id = lookup(j0 + 2 * KT);
         }
-        const uint8_t* kt = lds + buf * 2 * TILE;
-        const uint8_t* vt = kt + TILE;
-        if (j0 >= max(p_wave_last + 1, pre)) continue;       // nothing of the tile is seen by the wave's rows
+        if (j0 >= max(p_wave_last + 1, pre) || poisoned) return;      // nothing of the tile is seen by the wave's rows
         f32x16 s[KB];
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
-            const int row = b * 32 + c32;
-            u32x4 kf[QS];
 #pragma unroll
-            for (int k = 0; k < QS; ++k)
-                kf[k] = *reinterpret_cast<const u32x4*>(kt + row * (DP * 2) + ((2 * k + h32) ^ Shape::turn(row)) * 16);
-#pragma unroll
-            for (int k = 0; k < QS; ++k) s[b] = mfma32<BF16>(kf[k], q[k], s[b]);
+            for (int k = 0; k < QS; ++k) {
+                u32x4 kf = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(ka[k & 7] + K0 + b * 32 * DP * 2 + (k >> 3) * 256);
+                if (!EXACT) kf &= (2 * k + h32) * 8 < dim ? ~0u : 0u;
+                s[b] = mfma32<BF16>(kf, q[k], s[b]);
+            }
         }
         if constexpr (FEAT) {
 #pragma unroll
@@ -812,13 +855,15 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[b][e] = (sees >> (8 * (e >> 2) + (e & 3)) & 1) ? s[b][e] : -INFINITY;
             }
-            uint32_t found = 0;
-            for (int o = lane * 16; o < TILE; o += 1024) found |= odd_bits<BF16>(*reinterpret_cast<const u32x4*>(vt + o));
             // A masked tile with infinities or NaN in V: 0 times them would reach
             // rows that do not see their key.  The wave's rows are done another way.
-            poisoned |= __ballot(found != 0) != 0;
+            uint32_t found = 0;
+#pragma unroll 4
+            for (int o = lane * 16; o < TILE; o += 1024)
+                found |= odd_bits<BF16>(*reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((lds_ptr)lds + V0 + o));
+            poisoned = __ballot(found != 0) != 0;
+            if (poisoned) return;
         }
-        if (poisoned) continue;
         float top = s[0][0];
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -827,7 +872,7 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
         top = max_across32(top);
         if (__ballot(top * c > m * c + 8.f || m == -INFINITY) != 0) {
             const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
-            const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - base) * c);
+            const float keep = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - base) * c);
             m = m_new;
             l *= keep;
 #pragma unroll
@@ -835,32 +880,21 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
         u32x4 pr[2 * KB];
-        f32x8 sum;                               // eight short chains instead of one long one
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 f32x8 pe;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    pe[e] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * half + e], c, -mc));
-                    sum[e] += pe[e];
-                }
+                for (int e = 0; e < 8; ++e) pe[e] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * half + e], c, -mc));
                 pr[2 * b + half] = round8<BF16>(pe);
+                l = add_pairs<BF16>(pr[2 * b + half], l);
             }
-        l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
         // V^T: among each 16 lanes, four keys by 16 columns per read
         auto v_frag = [&](int k, int d) -> u32x4 {
-            uint2 part[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int row = 16 * k + 8 * y + 4 * h32 + ((lane & 15) >> 2);
-                const int piece = 4 * d + ((lane >> 4 & 1) << 1) + ((lane & 3) >> 1);
-                part[y] = read_transposed(vt + row * (DP * 2) + (piece ^ Shape::turn(row)) * 16 + (lane & 1) * 8);
-            }
-            return u32x4{part[0].x, part[0].y, part[1].x, part[1].y};
+            const uint2 x = read_transposed(va[0][d & 3] + V0 + 16 * k * DP * 2 + (d >> 2) * 256);
+            const uint2 y = read_transposed(va[1][d & 3] + V0 + 16 * k * DP * 2 + (d >> 2) * 256);
+            return u32x4{x.x, x.y, y.x, y.y};
         };
         u32x4 vf[2][DB];                         // one step of 16 keys ahead
 #pragma unroll
@@ -874,6 +908,10 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
 #pragma unroll
             for (int d = 0; d < DB; ++d) acc[d] = mfma32<BF16>(vf[k & 1][d], pr[k], acc[d]);
         }
+    };
+    for (int t = 0; t < ntiles; t += 2) {
+        step(std::integral_constant<int, 0>{}, t);
+        if (t + 1 < ntiles) step(std::integral_constant<int, 1>{}, t + 1);
     }
     l = sum_across32(l);
     if (threadIdx.x == 0 && *gap != 0) raise(p.status);
@@ -913,7 +951,7 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
 }
 
 template <int DP, bool BF16, bool EXACT, bool FEAT>
-__global__ __launch_bounds__(256, 2) void attention_chunk_kernel(AttnParams p, Cut cut) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attention_chunk_kernel(AttnParams p, Cut cut) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[ChunkShape<DP>::LDS];
     chunk_group<DP, BF16, EXACT, FEAT>(p, cut, blockIdx.x, lds);
 }
@@ -922,7 +960,7 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(AttnParams p, C
 // workgroups that wait for the matrix units share each CU.  Blocks of eight
 // neighbours (one per XCD) are all of one kind, the kinds spread evenly.
 template <int DP, bool BF16, bool EXACT, bool FEAT>
-__global__ __launch_bounds__(256, 2) void attention_mixed_kernel(AttnParams p, Partial part, Cut cut) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attention_mixed_kernel(AttnParams p, Partial part, Cut cut) {
     constexpr int LDS = ChunkShape<DP>::LDS > kRowsLds<DP, 1> ? ChunkShape<DP>::LDS : kRowsLds<DP, 1>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
     const int64_t b = blockIdx.x >> 3, tiles = (cut.tile_groups + 7) >> 3, all = tiles + ((cut.row_groups + 7) >> 3);
