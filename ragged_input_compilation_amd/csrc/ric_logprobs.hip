@@ -1,26 +1,51 @@
 // Log probabilities of given tokens, their rank, the row's entropy and the top
-// alternatives.  With m = max x, S = sum e^(x-m) and W = sum e^(x-m) (x-m):
+// alternatives.  With a reference m (the row's maximum, or a value up to 2^8 times
+// less likely), S = sum e^(x-m) and W = sum e^(x-m) (x-m):
 //     logprob = x_t - m - ln S,   entropy = ln S - W / S
-// (both terms of the entropy are >= 0, so nothing cancels).  Sums are float32.
+// Sums are float32, per lane, then across lanes, waves and pieces in a fixed order.
 //
 // Tokens are ordered by (logit descending, id ascending), which a 64-bit key
 // holds: the logit's bits mapped to an increasing unsigned number above the
 // complement of the id.  -0 counts as +0, a NaN lies above everything.
+//
+// Bound by reading the logits once: one pass, 16 bytes per lane and load, the next
+// block's loads in flight while a block is summed.  Rows are cut into pieces,
+// one workgroup each, where there are few of them.
 #include <algorithm>
 
 #include "ric_internal.h"
 
 namespace ric {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned long long u64;
+
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kVectors = 4;                  // loads of 16 bytes per lane and block
 
-__device__ __forceinline__ float load_logit(const uint8_t* row, int dtype, int64_t i) {
-    if (dtype == 2) return reinterpret_cast<const float*>(row)[i];
+struct Piece {                               // one piece of a row
+    float m, S, W;                           // sums relative to m, W in units of log2
+    int above;                               // tokens ordered before the target
+};
+
+template <int DT>
+__device__ __forceinline__ float load_logit(const uint8_t* row, int64_t i) {
+    if constexpr (DT == 2) return reinterpret_cast<const float*>(row)[i];
     const uint16_t h = reinterpret_cast<const uint16_t*>(row)[i];
-    if (dtype == 1) return __uint_as_float((uint32_t)h << 16);
+    if constexpr (DT == 1) return __uint_as_float((uint32_t)h << 16);
+    return (float)__builtin_bit_cast(_Float16, h);
+}
+
+// Element e of a 16-byte vector.
+template <int DT>
+__device__ __forceinline__ float element(u32x4 v, int e) {
+    if constexpr (DT == 2) return __uint_as_float(v[e]);
+    const uint32_t two = v[e >> 1];
+    if constexpr (DT == 1) return __uint_as_float((e & 1) ? two & 0xffff0000u : two << 16);
+    const uint16_t h = (uint16_t)((e & 1) ? two >> 16 : two);
     return (float)__builtin_bit_cast(_Float16, h);
 }
 
@@ -29,91 +54,370 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t b = __float_as_uint(x + 0.f);
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ u64 key_of(float x, int id) { return (u64)ordered(x) << 32 | (uint32_t)~id; }
+__device__ __forceinline__ int id_of(u64 key) { return (int)~(uint32_t)key; }
 
-}  // namespace
+__device__ __forceinline__ u64 read_lane(u64 x, int lane) {
+    return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+}
 
-// One workgroup per row, the row read once per output it takes (simple form).
-__global__ __launch_bounds__(256) void logprobs_simple_kernel(LogprobParams p) {
-    __shared__ float fs[4];
-    __shared__ unsigned long long ks[4];
-    __shared__ int cs[4];
-    const int r = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int count = p.dev_count != nullptr ? min(p.max_rows, *p.dev_count) : p.max_rows;
-    if (r >= count) return;
-    const uint8_t* row = p.logits + (int64_t)r * p.row_stride;
-    auto block_sum = [&](float x) {
-        for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-        if (lane == 0) fs[w] = x;
+// A wave's best keys so far, in descending order over its lanes (0: none).
+__device__ __forceinline__ void insert(u64& best, u64 key) {
+    const int at = __popcll(__ballot(best > key));
+    constexpr int kWaveShr1 = 0x138;
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)best, kWaveShr1, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(best >> 32), kWaveShr1, 0xf, 0xf, false);
+    const int lane = threadIdx.x & 63;
+    best = lane < at ? best : lane == at ? key : ((u64)hi << 32 | lo);
+}
+
+// Joins two descending lists: the larger of each lane and the other list's mirror
+// holds the best 64 as a bitonic sequence, which six exchanges sort.
+__device__ __forceinline__ u64 join(u64 a, u64 b) {
+    const int lane = threadIdx.x & 63;
+    u64 x = max(a, (u64)__shfl_xor(b, 63));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        const u64 y = __shfl_xor(x, o);
+        x = (lane & o) ? min(x, y) : max(x, y);
+    }
+    return x;
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    return x;
+}
+
+// Adds piece b to piece a.
+__device__ __forceinline__ void add(Piece& a, const Piece& b) {
+    const float m = fmaxf(a.m, b.m), base = m == -INFINITY ? 0.f : m;
+    // e^(x-m) (x-m) moves to a new reference as f (W + d S)
+    const float da = a.m == -INFINITY ? 0.f : (a.m - base) * kLog2e, db = b.m == -INFINITY ? 0.f : (b.m - base) * kLog2e;
+    const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
+    // a reference so far below that its weights vanish has nothing to move
+    a.W = (fa == 0.f ? 0.f * a.S : fa * fmaf(da, a.S, a.W)) + (fb == 0.f ? 0.f * b.S : fb * fmaf(db, b.S, b.W));
+    a.S = a.S * fa + b.S * fb;
+    a.m = m;
+    a.above += b.above;
+}
+
+// A row with NaN or infinities above: every log probability is NaN, the order is
+// found token by token, one pass per alternative.  256 threads.
+template <int DT>
+__device__ void broken_row(const LogprobParams& p, int r, const uint8_t* row, u64* shared) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    auto block = [&](u64 k, bool sum) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const u64 y = __shfl_xor(k, o);
+            k = sum ? k + y : max(k, y);
+        }
         __syncthreads();
-        const float t = (fs[0] + fs[1]) + (fs[2] + fs[3]);
+        if (lane == 0) shared[w] = k;
         __syncthreads();
-        return t;
-    };
-    auto block_key = [&](unsigned long long k) {
-        for (int o = 32; o > 0; o >>= 1) k = max(k, (unsigned long long)__shfl_xor(k, o));
-        if (lane == 0) ks[w] = k;
-        __syncthreads();
-        const unsigned long long t = max(max(ks[0], ks[1]), max(ks[2], ks[3]));
-        __syncthreads();
-        return t;
+        return sum ? shared[0] + shared[1] + shared[2] + shared[3] : max(max(shared[0], shared[1]), max(shared[2], shared[3]));
     };
     const int target = p.targets != nullptr ? p.targets[r] : -1;
     const bool has = target >= 0 && target < p.vocab;
-    const float xt = has ? load_logit(row, p.dtype, target) : 0.f;
-    const unsigned long long kt = has ? ((unsigned long long)ordered(xt) << 32) | (uint32_t)~target : 0;
-    unsigned long long best = 0;
-    int above = 0;
-    for (int i = threadIdx.x; i < p.vocab; i += 256) {
-        const unsigned long long k = ((unsigned long long)ordered(load_logit(row, p.dtype, i)) << 32) | (uint32_t)~i;
-        best = max(best, k);
-        above += has && k > kt;
-    }
-    best = block_key(best);
-    const float m = load_logit(row, p.dtype, (int)~(uint32_t)best);
-    const bool none = m == -INFINITY;
-    float S = 0.f, W = 0.f;
-    for (int i = threadIdx.x; i < p.vocab; i += 256) {
-        // 0 * -inf has no place in W: below -256 the weight is 0 already
-        const float d = fmaxf(load_logit(row, p.dtype, i) - m, -256.f), e = __builtin_amdgcn_exp2f(d * kLog2e);
-        S += e;
-        W += e * d;
-    }
-    S = block_sum(S);
-    W = block_sum(W);
-    for (int o = 32; o > 0; o >>= 1) above += __shfl_xor(above, o);
-    if (lane == 0) cs[w] = above;
-    __syncthreads();
-    const float lnS = __builtin_amdgcn_logf(S) * kLn2;
-    auto logp = [&](float x) { return none ? -INFINITY : (x - m) - lnS; };
+    const u64 kt = has ? key_of(load_logit<DT>(row, target), target) : 0;
+    u64 above = 0, last = ~0ull;
+    for (int i = threadIdx.x; i < p.vocab; i += 256) above += has && key_of(load_logit<DT>(row, i), i) > kt;
+    above = block(above, true);
     if (threadIdx.x == 0) {
         if (p.targets != nullptr) {
-            p.logprob[r] = has ? logp(xt) : 0.f;
-            p.rank[r] = has ? 1 + cs[0] + cs[1] + cs[2] + cs[3] : 0;
-            if (target >= p.vocab && p.status != nullptr) atomicAdd(p.status, 1);
+            p.logprob[r] = has ? NAN : 0.f;
+            p.rank[r] = has ? 1 + (int)above : 0;
         }
-        if (p.entropy != nullptr) p.entropy[r] = none ? 0.f : lnS - W / S;
+        if (p.entropy != nullptr) p.entropy[r] = NAN;
     }
-    unsigned long long last = ~0ull;
     for (int k = 0; k < p.top_k; ++k) {
-        unsigned long long b = 0;
+        u64 b = 0;
         for (int i = threadIdx.x; i < p.vocab; i += 256) {
-            const unsigned long long c = ((unsigned long long)ordered(load_logit(row, p.dtype, i)) << 32) | (uint32_t)~i;
+            const u64 c = key_of(load_logit<DT>(row, i), i);
             if (c < last) b = max(b, c);
         }
-        last = block_key(b);
+        last = block(b, false);
         if (threadIdx.x == 0) {
-            const int id = (int)~(uint32_t)last;
-            p.top_ids[(int64_t)r * p.top_k + k] = id;
-            p.top_logprobs[(int64_t)r * p.top_k + k] = logp(load_logit(row, p.dtype, id));
+            p.top_ids[(int64_t)r * p.top_k + k] = id_of(last);
+            p.top_logprobs[(int64_t)r * p.top_k + k] = NAN;
         }
     }
 }
 
-size_t logprobs_workspace(int32_t, int32_t, int32_t) { return 0; }
+// Writes row r from its whole piece and best keys; called by 256 threads, the
+// keys in the lanes of the first wave.
+template <int DT>
+__device__ __forceinline__ void finish_row(const LogprobParams& p, int r, const uint8_t* row, const Piece& whole, u64 best,
+                                           u64* shared) {
+    const int target = p.targets != nullptr ? p.targets[r] : -1;
+    if (threadIdx.x == 0 && target >= p.vocab && p.status != nullptr) atomicAdd(p.status, 1);
+    if (whole.S != whole.S) {
+        broken_row<DT>(p, r, row, shared);
+        return;
+    }
+    if (threadIdx.x >= 64) return;
+    const bool none = whole.m == -INFINITY;      // no token has a probability
+    const float lnS = logf(whole.S);
+    if (threadIdx.x == 0) {
+        const bool has = target >= 0 && target < p.vocab;
+        if (p.targets != nullptr) {
+            p.logprob[r] = !has ? 0.f : none ? -INFINITY : (load_logit<DT>(row, target) - whole.m) - lnS;
+            p.rank[r] = has ? 1 + whole.above : 0;
+        }
+        if (p.entropy != nullptr) p.entropy[r] = none ? 0.f : lnS - whole.W * kLn2 / whole.S;
+    }
+    if ((int)threadIdx.x < p.top_k) {
+        const int64_t at = (int64_t)r * p.top_k + threadIdx.x;
+        p.top_ids[at] = id_of(best);
+        p.top_logprobs[at] = none ? -INFINITY : (from_ordered((uint32_t)(best >> 32)) - whole.m) - lnS;
+    }
+}
 
-hipError_t launch_logprobs(const LogprobParams& p, void*, hipStream_t s) {
-    hipLaunchKernelGGL(logprobs_simple_kernel, dim3(p.max_rows), dim3(256), 0, s, p);
+}  // namespace
+
+// One piece of a row per workgroup: its 16-byte vectors in blocks of 64 lanes x
+// kVectors, dealt to the four waves in turn, so that a wave meets rising ids.
+// A row may start at any element: those before the first whole vector go to the
+// first piece's first wave before its blocks, those behind the last to the last
+// piece's after them.
+//   m: a wave takes its first block's maximum, and a new one where a block exceeds
+//     it by more than 2^8, so hardly any block rescales.
+//   top: a wave keeps its best keys sorted over its lanes; a block is looked at again
+//     only if its maximum passes the last of them, which happens k ln(n / k) times
+//     over n unsorted tokens.  The first block is entered above the k-th largest of
+//     its lanes' maxima.
+//   rank: a compare and a count of the lanes per 64 tokens; equal logits count
+//     before the target's id.
+template <int DT>
+__global__ __launch_bounds__(256) void logprobs_kernel(LogprobParams p, int pieces, Piece* part, u64* part_keys) {
+    constexpr int VE = DT == 2 ? 4 : 8;          // elements per vector
+    constexpr int BLOCK = 64 * kVectors;         // vectors per block
+    __shared__ Piece waves[4];
+    __shared__ u64 keys[4][64];
+    const int r = blockIdx.x / pieces, piece = blockIdx.x - r * pieces;
+    const int count = p.dev_count != nullptr ? min(p.max_rows, *p.dev_count) : p.max_rows;
+    if (r >= count) return;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint8_t* row = p.logits + (int64_t)r * p.row_stride;
+    const int size = DT == 2 ? 4 : 2;
+    const int head = min(p.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / size);
+    const int vectors = (p.vocab - head) / VE, tail = p.vocab - head - vectors * VE;
+    const u32x4* body = reinterpret_cast<const u32x4*>(row + (int64_t)head * size);
+    const int blocks = (vectors + BLOCK - 1) / BLOCK;
+    const int b0 = (int)((int64_t)blocks * piece / pieces), b1 = (int)((int64_t)blocks * (piece + 1) / pieces);
+    const int target = p.targets != nullptr ? p.targets[r] : -1;
+    const bool has = target >= 0 && target < p.vocab;
+    const float xt = has ? load_logit<DT>(row, target) : INFINITY;
+    const int K = p.top_k;
+
+    Piece mine{-INFINITY, 0.f, 0.f, 0};          // S and W are the lane's own
+    u64 best = 0;
+    float floor_x = -INFINITY;                   // value of the K-th best key
+    bool open = K > 0;                           // fewer than K keys yet
+    auto enter = [&](float x, int id, bool maybe) {      // per lane, all lanes at once
+        for (u64 todo = __ballot(maybe); todo != 0; todo &= todo - 1) {
+            const int from = __ffsll(todo) - 1;
+            const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), from));
+            const u64 key = key_of(v, __builtin_amdgcn_readlane(id, from));
+            const u64 kth = read_lane(best, K - 1);
+            if (key > kth) {
+                insert(best, key);
+                const u64 now = read_lane(best, K - 1);
+                open = now == 0;
+                floor_x = open ? -INFINITY : from_ordered((uint32_t)(now >> 32));
+            }
+        }
+    };
+    auto weigh = [&](float x) {
+        const float d = (x - (mine.m == -INFINITY ? 0.f : mine.m)) * kLog2e;
+        const float e = __builtin_amdgcn_exp2f(d);
+        mine.S += e;
+        mine.W = fmaf(e, fmaxf(d, -300.f), mine.W);      // 0 * -inf has no place in W
+    };
+    auto refer = [&](float top) {                // `top`: the wave's largest new logit
+        if (top <= mine.m + 8.f * kLn2 || top == -INFINITY) return;
+        const float d = mine.m == -INFINITY ? 0.f : (mine.m - top) * kLog2e, f = __builtin_amdgcn_exp2f(d);
+        mine.W = f == 0.f ? 0.f * mine.S : f * fmaf(d, mine.S, mine.W);
+        mine.S *= f;
+        mine.m = top;
+    };
+    auto wave_max = [&](float x) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+        return x;
+    };
+    auto loose = [&](int first, int n) {         // n < 64 single elements
+        const bool in = lane < n;
+        const float x = in ? load_logit<DT>(row, first + lane) : -INFINITY;
+        refer(wave_max(x));
+        if (in) weigh(x);
+        mine.above += __popcll(__ballot(in && has && (x > xt || (x == xt && first + lane < target))));
+        if (K > 0) enter(x, first + lane, in && (open || x > floor_x));
+    };
+
+    if (w == 0 && piece == 0 && head > 0) loose(0, head);
+    u32x4 next[kVectors];
+    auto request = [&](int b) {
+#pragma unroll
+        for (int u = 0; u < kVectors; ++u) {
+            const int v = min(b * BLOCK + u * 64 + lane, vectors - 1);
+            next[u] = __builtin_nontemporal_load(body + v);
+        }
+    };
+    if (b0 + w < b1) request(b0 + w);
+    bool first = true;
+    for (int b = b0 + w; b < b1; b += 4) {
+        u32x4 now[kVectors];
+#pragma unroll
+        for (int u = 0; u < kVectors; ++u) now[u] = next[u];
+        if (b + 4 < b1) request(b + 4);
+        if ((b + 1) * BLOCK > vectors) {         // the row's last block: lanes past its end see nothing
+#pragma unroll
+            for (int u = 0; u < kVectors; ++u)
+                if (b * BLOCK + u * 64 + lane >= vectors) {
+                    const uint32_t low = DT == 2 ? 0xff800000u : DT == 1 ? 0xff80ff80u : 0xfc00fc00u;
+                    now[u] = u32x4{low, low, low, low};
+                }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) top = fmaxf(top, element<DT>(now[u], e));
+        if (__ballot(top > mine.m + 8.f * kLn2) != 0) refer(wave_max(top));
+#pragma unroll
+        for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) weigh(element<DT>(now[u], e));
+        if (has) {
+            const int id0 = head + b * BLOCK * VE;
+            if (target < id0) {
+#pragma unroll
+                for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) mine.above += __popcll(__ballot(element<DT>(now[u], e) > xt));
+            } else if (target >= id0 + BLOCK * VE) {
+#pragma unroll
+                for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) mine.above += __popcll(__ballot(element<DT>(now[u], e) >= xt));
+            } else {
+#pragma unroll
+                for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float x = element<DT>(now[u], e);
+                        mine.above += __popcll(__ballot(x > xt || (x == xt && id0 + (u * 64 + lane) * VE + e < target)));
+                    }
+            }
+        }
+        if (K > 0) {
+            // Tokens of earlier blocks have lower ids: this block's must exceed their
+            // K-th.  Among its own an equal one may still have the lower id.
+            float enter_at = -INFINITY;
+            const float before = floor_x;
+            const bool any = open;
+            const bool fill = first && open && (b + 1) * BLOCK <= vectors;
+            if (fill) {
+                // 64 lanes' maxima, sorted: at least K tokens reach the K-th of them
+                float x = top;
+#pragma unroll
+                for (int k = 2; k <= 64; k <<= 1)
+#pragma unroll
+                    for (int o = k >> 1; o > 0; o >>= 1) {
+                        const float y = __shfl_xor(x, o);
+                        x = ((lane & o) == 0) == ((lane & k) == 0) ? fmaxf(x, y) : fminf(x, y);
+                    }
+                enter_at = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), K - 1));
+            }
+            if (any || __ballot(top > before) != 0) {
+#pragma unroll
+                for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const int v = b * BLOCK + u * 64 + lane;
+                        const float x = element<DT>(now[u], e);
+                        const bool maybe = v < vectors && x >= floor_x && (any ? x >= enter_at : x > before);
+                        if (__ballot(maybe) != 0) enter(x, head + v * VE + e, maybe);
+                    }
+            }
+            first = false;
+        }
+    }
+    if (w == 0 && piece == pieces - 1 && tail > 0) loose(head + vectors * VE, tail);
+
+    mine.S = wave_sum(mine.S);
+    mine.W = wave_sum(mine.W);
+    if (lane == 0) waves[w] = mine;
+    keys[w][lane] = best;
+    __syncthreads();
+    Piece whole = waves[0];
+    for (int k = 1; k < 4; ++k) add(whole, waves[k]);
+    if (w == 0 && K > 0)
+        for (int k = 1; k < 4; ++k) best = join(best, keys[k][lane]);
+    if (pieces == 1) {
+        __syncthreads();
+        finish_row<DT>(p, r, row, whole, best, &keys[0][0]);
+        return;
+    }
+    if (w != 0) return;
+    const int64_t at = (int64_t)r * pieces + piece;
+    if (lane == 0) part[at] = whole;
+    if (lane < K) part_keys[at * K + lane] = best;
+}
+
+// Joins the pieces of a row, in order.
+template <int DT>
+__global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p, int pieces, const Piece* part, const u64* part_keys) {
+    __shared__ u64 shared[4];
+    const int r = blockIdx.x, lane = threadIdx.x & 63;
+    const int count = p.dev_count != nullptr ? min(p.max_rows, *p.dev_count) : p.max_rows;
+    if (r >= count) return;
+    Piece whole = part[(int64_t)r * pieces];
+    for (int k = 1; k < pieces; ++k) add(whole, part[(int64_t)r * pieces + k]);
+    u64 best = 0;
+    if (threadIdx.x < 64 && p.top_k > 0)
+        for (int k = 0; k < pieces; ++k)
+            best = join(best, lane < p.top_k ? part_keys[((int64_t)r * pieces + k) * p.top_k + lane] : 0);
+    finish_row<DT>(p, r, p.logits + (int64_t)r * p.row_stride, whole, best, shared);
+}
+
+namespace {
+
+// Pieces per row: enough workgroups to fill 256 CUs four times over, each with at
+// least 8192 logits.
+int pieces_of(int32_t max_rows, int32_t vocab) {
+    const int want = (1024 + max_rows - 1) / max_rows;
+    return std::max(1, std::min({want, vocab / 8192, 32}));
+}
+
+template <int DT>
+hipError_t launch(const LogprobParams& p, Piece* part, u64* keys, int pieces, hipStream_t s) {
+    hipLaunchKernelGGL(logprobs_kernel<DT>, dim3(p.max_rows * pieces), dim3(256), 0, s, p, pieces, part, keys);
+    if (pieces > 1) hipLaunchKernelGGL(logprobs_join_kernel<DT>, dim3(p.max_rows), dim3(256), 0, s, p, pieces, part, keys);
     return hipGetLastError();
+}
+
+}  // namespace
+
+size_t logprobs_workspace(int32_t max_rows, int32_t vocab, int32_t top_k) {
+    const int pieces = pieces_of(max_rows, vocab);
+    return pieces == 1 ? 0 : (size_t)max_rows * pieces * (sizeof(Piece) + 8 * (size_t)top_k);
+}
+
+hipError_t launch_logprobs(const LogprobParams& p, void* workspace, hipStream_t s) {
+    const int pieces = pieces_of(p.max_rows, p.vocab);
+    Piece* part = static_cast<Piece*>(workspace);
+    u64* keys = reinterpret_cast<u64*>(part + (int64_t)p.max_rows * pieces);
+    if (p.dtype == 2) return launch<2>(p, part, keys, pieces, s);
+    if (p.dtype == 1) return launch<1>(p, part, keys, pieces, s);
+    return launch<0>(p, part, keys, pieces, s);
 }
 
 }  // namespace ric
