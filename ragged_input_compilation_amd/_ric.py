@@ -475,7 +475,7 @@ def _page_args(src, dst, k_cache_ptrs, v_cache_ptrs):
     if len(k_cache_ptrs) != len(v_cache_ptrs):
         raise ValueError("pointer lists differ in length")
     L = len(k_cache_ptrs)
-    kc, vc = ((_vp * max(L, 1))(*[_vp(x) for x in lst]) for lst in (k_cache_ptrs, v_cache_ptrs))
+    kc, vc = ((_vp * max(L, 1))(*lst) for lst in (k_cache_ptrs, v_cache_ptrs))
     return (s, d, kc, vc), (s.shape[0], sp, dp, ctypes.cast(kc, ctypes.POINTER(_vp)),
                             ctypes.cast(vc, ctypes.POINTER(_vp)), L)
 

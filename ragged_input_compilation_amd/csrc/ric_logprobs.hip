@@ -57,6 +57,11 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float from_ordered(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
+// The next float below x (> -inf).
+__device__ __forceinline__ float lower_than(float x) {
+    const uint32_t o = ordered(x);
+    return from_ordered(o == 0x80000000u ? 0x7ffffffeu : o - 1);     // -0 is 0
+}
 __device__ __forceinline__ u64 key_of(float x, int id) { return (u64)ordered(x) << 32 | (uint32_t)~id; }
 __device__ __forceinline__ int id_of(u64 key) { return (int)~(uint32_t)key; }
 
@@ -190,16 +195,19 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, int r, const 
 //     it by more than 2^8, so hardly any block rescales.
 //   top: a wave keeps its best keys sorted over its lanes; a block is looked at again
 //     only if its maximum passes the last of them, which happens k ln(n / k) times
-//     over n unsorted tokens.  The first block is entered above the k-th largest of
-//     its lanes' maxima.
+//     over n unsorted tokens.  What passes is listed in LDS and entered one by one,
+//     or sorted and joined where it is many.  The first block is entered above the
+//     k-th largest of its lanes' maxima.
 //   rank: a compare and a count of the lanes per 64 tokens; equal logits count
-//     before the target's id.
+//     before the target's id, so blocks before it compare with the next lower float.
+// 60 registers: eight workgroups share a CU and keep its loads in flight.
 template <int DT>
-__global__ __launch_bounds__(256) void logprobs_kernel(LogprobParams p, int pieces, Piece* part, u64* part_keys) {
+__global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int pieces, Piece* part, u64* part_keys) {
     constexpr int VE = DT == 2 ? 4 : 8;          // elements per vector
     constexpr int BLOCK = 64 * kVectors;         // vectors per block
+    constexpr int LIST = 256, FULL = 192;        // keys listed per wave; more are entered from memory
     __shared__ Piece waves[4];
-    __shared__ u64 keys[4][64];
+    __shared__ u64 lists[4][LIST];
     const int r = blockIdx.x / pieces, piece = blockIdx.x - r * pieces;
     const int count = p.dev_count != nullptr ? min(p.max_rows, *p.dev_count) : p.max_rows;
     if (r >= count) return;
@@ -214,25 +222,52 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobParams p, int piec
     const int target = p.targets != nullptr ? p.targets[r] : -1;
     const bool has = target >= 0 && target < p.vocab;
     const float xt = has ? load_logit<DT>(row, target) : INFINITY;
+    // x >= xt is x > lower (for xt = -inf, every x)
+    const float lower = xt == -INFINITY ? xt : lower_than(xt);
     const int K = p.top_k;
 
     Piece mine{-INFINITY, 0.f, 0.f, 0};          // S and W are the lane's own
     u64 best = 0;
     float floor_x = -INFINITY;                   // value of the K-th best key
     bool open = K > 0;                           // fewer than K keys yet
-    auto enter = [&](float x, int id, bool maybe) {      // per lane, all lanes at once
-        for (u64 todo = __ballot(maybe); todo != 0; todo &= todo - 1) {
-            const int from = __ffsll(todo) - 1;
-            const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), from));
-            const u64 key = key_of(v, __builtin_amdgcn_readlane(id, from));
-            const u64 kth = read_lane(best, K - 1);
-            if (key > kth) {
-                insert(best, key);
-                const u64 now = read_lane(best, K - 1);
-                open = now == 0;
-                floor_x = open ? -INFINITY : from_ordered((uint32_t)(now >> 32));
+    int listed = 0;
+    auto settle = [&]() {
+        const u64 kth = read_lane(best, K - 1);
+        open = kth == 0;
+        floor_x = open ? -INFINITY : from_ordered((uint32_t)(kth >> 32));
+    };
+    auto enter = [&](u64 keys, u64 todo) {       // the lanes' keys, one after the other
+        for (; todo != 0; todo &= todo - 1) {
+            const u64 key = read_lane(keys, __ffsll(todo) - 1);
+            if (key > read_lane(best, K - 1)) insert(best, key);
+        }
+    };
+    auto list = [&](u64 key, bool maybe, u64 lanes) {
+        const int at = listed + __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
+        if (maybe) lists[w][at] = key;
+        listed += __popcll(lanes);
+    };
+    auto drain = [&]() {
+        __builtin_amdgcn_wave_barrier();
+        for (int at = 0; at < listed; at += 64) {
+            const int n = min(64, listed - at);
+            u64 keys = lane < n ? lists[w][at + lane] : 0;
+            if (n > 12) {
+#pragma unroll 1
+                for (int k = 2; k <= 64; k <<= 1)
+#pragma unroll 1
+                    for (int o = k >> 1; o > 0; o >>= 1) {
+                        const u64 y = __shfl_xor(keys, o);
+                        keys = ((lane & o) == 0) == ((lane & k) == 0) ? max(keys, y) : min(keys, y);
+                    }
+                best = join(best, keys);
+            } else {
+                enter(keys, __ballot(lane < n));
             }
         }
+        listed = 0;
+        settle();
+        __builtin_amdgcn_wave_barrier();
     };
     auto weigh = [&](float x) {
         const float d = (x - (mine.m == -INFINITY ? 0.f : mine.m)) * kLog2e;
@@ -252,32 +287,24 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobParams p, int piec
         for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
         return x;
     };
-    auto loose = [&](int first, int n) {         // n < 64 single elements
+    auto loose = [&](int first, int n) {         // n < 8 single elements
         const bool in = lane < n;
-        const float x = in ? load_logit<DT>(row, first + lane) : -INFINITY;
+        const int id = first + lane;
+        const float x = in ? load_logit<DT>(row, id) : -INFINITY;
         refer(wave_max(x));
         if (in) weigh(x);
-        mine.above += __popcll(__ballot(in && has && (x > xt || (x == xt && first + lane < target))));
-        if (K > 0) enter(x, first + lane, in && (open || x > floor_x));
+        mine.above += __popcll(__ballot(in && has && (x > xt || (x == xt && id < target))));
+        if (K > 0) list(key_of(x, id), in, __ballot(in));
     };
 
     if (w == 0 && piece == 0 && head > 0) loose(0, head);
-    u32x4 next[kVectors];
-    auto request = [&](int b) {
-#pragma unroll
-        for (int u = 0; u < kVectors; ++u) {
-            const int v = min(b * BLOCK + u * 64 + lane, vectors - 1);
-            next[u] = __builtin_nontemporal_load(body + v);
-        }
-    };
-    if (b0 + w < b1) request(b0 + w);
-    bool first = true;
     for (int b = b0 + w; b < b1; b += 4) {
         u32x4 now[kVectors];
 #pragma unroll
-        for (int u = 0; u < kVectors; ++u) now[u] = next[u];
-        if (b + 4 < b1) request(b + 4);
-        if ((b + 1) * BLOCK > vectors) {         // the row's last block: lanes past its end see nothing
+        for (int u = 0; u < kVectors; ++u)
+            now[u] = __builtin_nontemporal_load(body + min(b * BLOCK + u * 64 + lane, vectors - 1));
+        const bool whole_block = (b + 1) * BLOCK <= vectors;
+        if (!whole_block) {                      // the row's last: lanes past its end see nothing
 #pragma unroll
             for (int u = 0; u < kVectors; ++u)
                 if (b * BLOCK + u * 64 + lane >= vectors) {
@@ -295,75 +322,101 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobParams p, int piec
         for (int u = 0; u < kVectors; ++u)
 #pragma unroll
             for (int e = 0; e < VE; ++e) weigh(element<DT>(now[u], e));
+        const int id0 = head + b * BLOCK * VE;   // the block's first id
         if (has) {
-            const int id0 = head + b * BLOCK * VE;
-            if (target < id0) {
+            if (target < id0 || (target >= id0 + BLOCK * VE && xt != -INFINITY)) {
+                const float past = target < id0 ? xt : lower;
 #pragma unroll
                 for (int u = 0; u < kVectors; ++u)
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) mine.above += __popcll(__ballot(element<DT>(now[u], e) > xt));
+                    for (int e = 0; e < VE; ++e) mine.above += __popcll(__ballot(element<DT>(now[u], e) > past));
             } else if (target >= id0 + BLOCK * VE) {
-#pragma unroll
-                for (int u = 0; u < kVectors; ++u)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) mine.above += __popcll(__ballot(element<DT>(now[u], e) >= xt));
+                mine.above += BLOCK * VE;        // every token is at least -inf
             } else {
-#pragma unroll
-                for (int u = 0; u < kVectors; ++u)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float x = element<DT>(now[u], e);
-                        mine.above += __popcll(__ballot(x > xt || (x == xt && id0 + (u * 64 + lane) * VE + e < target)));
-                    }
+#pragma unroll 1
+                for (int k = lane; k < BLOCK * VE; k += 64) {
+                    const int id = id0 + k;
+                    const float x = id < head + vectors * VE ? load_logit<DT>(row, id) : -INFINITY;
+                    mine.above += __popcll(__ballot(id < head + vectors * VE && (x > xt || (x == xt && id < target))));
+                }
             }
         }
-        if (K > 0) {
-            // Tokens of earlier blocks have lower ids: this block's must exceed their
-            // K-th.  Among its own an equal one may still have the lower id.
-            float enter_at = -INFINITY;
-            const float before = floor_x;
-            const bool any = open;
-            const bool fill = first && open && (b + 1) * BLOCK <= vectors;
-            if (fill) {
+        if (K > 0 && (open || __ballot(top > floor_x) != 0)) {
+            // Tokens of earlier blocks have lower ids: these must exceed their K-th.
+            float reach = open ? -INFINITY : floor_x;
+            const bool equal = open;
+            if (open && whole_block) {
                 // 64 lanes' maxima, sorted: at least K tokens reach the K-th of them
                 float x = top;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
+#pragma unroll 1
                     for (int o = k >> 1; o > 0; o >>= 1) {
                         const float y = __shfl_xor(x, o);
                         x = ((lane & o) == 0) == ((lane & k) == 0) ? fmaxf(x, y) : fminf(x, y);
                     }
-                enter_at = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), K - 1));
+                reach = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), K - 1));
             }
-            if (any || __ballot(top > before) != 0) {
+            // the lane's passing tokens, as bits; each is read again and listed
+            const bool all = equal && reach == -INFINITY;
+            const float over = equal ? lower_than(reach) : reach;
+            uint32_t passing = 0;
+#pragma unroll
+            for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    passing |= (all || element<DT>(now[u], e) > over) ? 1u << (u * VE + e) : 0u;
+            if (!whole_block) {
 #pragma unroll
                 for (int u = 0; u < kVectors; ++u)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const int v = b * BLOCK + u * 64 + lane;
-                        const float x = element<DT>(now[u], e);
-                        const bool maybe = v < vectors && x >= floor_x && (any ? x >= enter_at : x > before);
-                        if (__ballot(maybe) != 0) enter(x, head + v * VE + e, maybe);
-                    }
+                    if (b * BLOCK + u * 64 + lane >= vectors) passing &= ~(((1u << VE) - 1u) << (u * VE));
             }
-            first = false;
+            bool many = false;
+            for (u64 lanes = __ballot(passing != 0); lanes != 0; lanes = __ballot(passing != 0)) {
+                many = listed > FULL;
+                if (many) break;
+                const int k = __ffs(passing) - 1;
+                const int id = id0 + ((k / VE) * 64 + lane) * VE + k % VE;
+                const bool in = passing != 0;
+                list(key_of(in ? load_logit<DT>(row, id) : 0.f, id), in, lanes);
+                passing &= passing - 1;
+            }
+            if (many) {                          // more than the list takes (rising or equal tokens)
+                listed = 0;
+#pragma unroll 1
+                for (int k = lane; k < BLOCK * VE; k += 64) {
+                    const int id = id0 + k;
+                    const float x = id < head + vectors * VE ? load_logit<DT>(row, id) : -INFINITY;
+                    const u64 key = key_of(x, id);
+                    enter(key, __ballot(id < head + vectors * VE && key > read_lane(best, K - 1)));
+                }
+                if (b == b0 && w == 0 && piece == 0 && head > 0) {       // listed before the block
+                    const u64 key = lane < head ? key_of(load_logit<DT>(row, lane), lane) : 0;
+                    enter(key, __ballot(lane < head));
+                }
+                settle();
+            } else if (listed > 0) {
+                drain();
+            }
         }
     }
     if (w == 0 && piece == pieces - 1 && tail > 0) loose(head + vectors * VE, tail);
+    if (listed > 0) drain();
 
     mine.S = wave_sum(mine.S);
     mine.W = wave_sum(mine.W);
     if (lane == 0) waves[w] = mine;
-    keys[w][lane] = best;
+    lists[w][lane] = best;
     __syncthreads();
     Piece whole = waves[0];
     for (int k = 1; k < 4; ++k) add(whole, waves[k]);
-    if (w == 0 && K > 0)
-        for (int k = 1; k < 4; ++k) best = join(best, keys[k][lane]);
+    if (w == 0 && K > 0) {
+#pragma unroll 1
+        for (int k = 1; k < 4; ++k) best = join(best, lists[k][lane]);
+    }
     if (pieces == 1) {
         __syncthreads();
-        finish_row<DT>(p, r, row, whole, best, &keys[0][0]);
+        finish_row<DT>(p, r, row, whole, best, &lists[0][0]);
         return;
     }
     if (w != 0) return;
@@ -372,19 +425,37 @@ __global__ __launch_bounds__(256) void logprobs_kernel(LogprobParams p, int piec
     if (lane < K) part_keys[at * K + lane] = best;
 }
 
-// Joins the pieces of a row, in order.
+// Joins the pieces of a row (at most 32): sums in a tree over the lanes, key lists
+// one after the other, the next one's load in flight.
 template <int DT>
 __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p, int pieces, const Piece* part, const u64* part_keys) {
     __shared__ u64 shared[4];
     const int r = blockIdx.x, lane = threadIdx.x & 63;
     const int count = p.dev_count != nullptr ? min(p.max_rows, *p.dev_count) : p.max_rows;
     if (r >= count) return;
-    Piece whole = part[(int64_t)r * pieces];
-    for (int k = 1; k < pieces; ++k) add(whole, part[(int64_t)r * pieces + k]);
-    u64 best = 0;
+    const u64* keys = part_keys + (int64_t)r * pieces * p.top_k;
+    const bool mine = threadIdx.x < 64 && lane < p.top_k;
+    u64 best = 0, next = mine ? keys[lane] : 0;
+    Piece whole{-INFINITY, 0.f, 0.f, 0};
+    if (lane < pieces) whole = part[(int64_t)r * pieces + lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Piece other{__shfl_xor(whole.m, o), __shfl_xor(whole.S, o), __shfl_xor(whole.W, o), __shfl_xor(whole.above, o)};
+        if (lane & o) {                          // the same operands in the same order on both sides
+            Piece sum = other;
+            add(sum, whole);
+            whole = sum;
+        } else {
+            add(whole, other);
+        }
+    }
+    whole = Piece{__shfl(whole.m, 0), __shfl(whole.S, 0), __shfl(whole.W, 0), __shfl(whole.above, 0)};
     if (threadIdx.x < 64 && p.top_k > 0)
-        for (int k = 0; k < pieces; ++k)
-            best = join(best, lane < p.top_k ? part_keys[((int64_t)r * pieces + k) * p.top_k + lane] : 0);
+        for (int k = 0; k < pieces; ++k) {
+            const u64 now = next;
+            next = mine && k + 1 < pieces ? keys[(int64_t)(k + 1) * p.top_k + lane] : 0;
+            best = k == 0 ? now : join(best, now);
+        }
     finish_row<DT>(p, r, p.logits + (int64_t)r * p.row_stride, whole, best, shared);
 }
 

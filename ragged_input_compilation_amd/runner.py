@@ -404,11 +404,15 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top_k:
 
 
 def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor]):
-    for t in [*kc, *vc]:
-        if not t.is_contiguous() or t.shape != kc[0].shape or t.dtype != kc[0].dtype:
-            raise ValueError("the layers' caches must be contiguous and alike")
-    nbytes = kc[0][0].numel() * kc[0].element_size() if kc else 0
-    return [t.data_ptr() for t in kc], [t.data_ptr() for t in vc], nbytes
+    """Addresses of the layers' caches and the bytes of a page."""
+    if not kc:
+        return [], [], 0
+    n, dtype = kc[0].numel(), kc[0].dtype
+    for lst in (kc, vc):
+        for t in lst:
+            if not t.is_contiguous() or t.dtype is not dtype or t.numel() != n:
+                raise ValueError("the layers' caches must be contiguous and alike")
+    return [t.data_ptr() for t in kc], [t.data_ptr() for t in vc], n // kc[0].shape[0] * kc[0].element_size()
 
 
 def copy_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
