@@ -24,7 +24,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kVectors = 4;                  // loads of 16 bytes per lane and block
+constexpr int kVectors = 2;                  // loads of 16 bytes per lane and block
 
 struct Piece {                               // one piece of a row
     float m, S, W;                           // sums relative to m, W in units of log2
@@ -62,12 +62,73 @@ __device__ __forceinline__ float lower_than(float x) {
     const uint32_t o = ordered(x);
     return from_ordered(o == 0x80000000u ? 0x7ffffffeu : o - 1);     // -0 is 0
 }
+// The next float above x (< inf).
+__device__ __forceinline__ float higher_than(float x) {
+    const uint32_t o = ordered(x);
+    return from_ordered(o == 0x7ffffffeu ? 0x80000000u : o + 1);
+}
 __device__ __forceinline__ u64 key_of(float x, int id) { return (u64)ordered(x) << 32 | (uint32_t)~id; }
 __device__ __forceinline__ int id_of(u64 key) { return (int)~(uint32_t)key; }
 
 __device__ __forceinline__ u64 read_lane(u64 x, int lane) {
     return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32 |
            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+}
+
+// The value of lane ^ O, in vector moves (an exchange through LDS takes several
+// times as long, and the sorts below are chains of them).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+    return __builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+template <int O>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+    constexpr int kQuad1032 = 0xb1, kQuad2301 = 0x4e, kQuad3210 = 0x1b, kMirror = 0x140, kHalfMirror = 0x141;
+    const int lane = threadIdx.x & 63;
+    if constexpr (O == 1) return dpp<kQuad1032>(x);
+    else if constexpr (O == 2) return dpp<kQuad2301>(x);
+    else if constexpr (O == 4) return dpp<kQuad3210>(dpp<kHalfMirror>(x));
+    else if constexpr (O == 8) return dpp<kHalfMirror>(dpp<kMirror>(x));
+    else if constexpr (O == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        return (lane & 16) ? r[0] : r[1];
+    } else if constexpr (O == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return (lane & 32) ? r[0] : r[1];
+    } else {
+        static_assert(O == 63);
+        return lane_xor<32>(lane_xor<16>(dpp<kMirror>(x)));
+    }
+}
+template <int O>
+__device__ __forceinline__ float lane_xor(float x) { return __uint_as_float(lane_xor<O>(__float_as_uint(x))); }
+template <int O>
+__device__ __forceinline__ u64 lane_xor(u64 x) {
+    return (u64)lane_xor<O>((uint32_t)(x >> 32)) << 32 | lane_xor<O>((uint32_t)x);
+}
+
+// One step of a bitonic sort: lanes O apart, descending where DESC.
+template <int O, class T>
+__device__ __forceinline__ T exchange(T x, bool larger) {
+    const T y = lane_xor<O>(x);
+    return larger == (y > x) ? y : x;
+}
+template <int K, int O, class T>
+__device__ __forceinline__ T sort_steps(T x) {
+    const int lane = threadIdx.x & 63;
+    x = exchange<O>(x, ((lane & O) == 0) == ((lane & K) == 0));
+    if constexpr (O > 1) return sort_steps<K, O / 2>(x);
+    else return x;
+}
+// The lanes' values in descending order.
+template <class T>
+__device__ __forceinline__ T sort64(T x) {
+    x = sort_steps<2, 1>(x);
+    x = sort_steps<4, 2>(x);
+    x = sort_steps<8, 4>(x);
+    x = sort_steps<16, 8>(x);
+    x = sort_steps<32, 16>(x);
+    return sort_steps<64, 32>(x);
 }
 
 // A wave's best keys so far, in descending order over its lanes (0: none).
@@ -83,20 +144,16 @@ __device__ __forceinline__ void insert(u64& best, u64 key) {
 // Joins two descending lists: the larger of each lane and the other list's mirror
 // holds the best 64 as a bitonic sequence, which six exchanges sort.
 __device__ __forceinline__ u64 join(u64 a, u64 b) {
-    const int lane = threadIdx.x & 63;
-    u64 x = max(a, (u64)__shfl_xor(b, 63));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const u64 y = __shfl_xor(x, o);
-        x = (lane & o) ? min(x, y) : max(x, y);
-    }
-    return x;
+    return sort_steps<64, 32>(max(a, lane_xor<63>(b)));
 }
 
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-    return x;
+    x += lane_xor<1>(x);
+    x += lane_xor<2>(x);
+    x += lane_xor<4>(x);
+    x += lane_xor<8>(x);
+    x += lane_xor<16>(x);
+    return x + lane_xor<32>(x);
 }
 
 // Adds piece b to piece a.
@@ -194,20 +251,22 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, int r, const 
 //   m: a wave takes its first block's maximum, and a new one where a block exceeds
 //     it by more than 2^8, so hardly any block rescales.
 //   top: a wave keeps its best keys sorted over its lanes; a block is looked at again
-//     only if its maximum passes the last of them, which happens k ln(n / k) times
-//     over n unsorted tokens.  What passes is listed in LDS and entered one by one,
-//     or sorted and joined where it is many.  The first block is entered above the
-//     k-th largest of its lanes' maxima.
+//     only if its maximum reaches the floor: the wave's own K-th key, or the least
+//     of the four waves' ceil(K / 4)-th, which K tokens of the row reach together.
+//     Over unsorted tokens that happens about K / 4 ln(n / K) times per wave.  What
+//     passes is entered one by one, or sorted and joined where it is many.  The first
+//     block is entered above the K-th largest of its lanes' maxima.
 //   rank: a compare and a count of the lanes per 64 tokens; equal logits count
 //     before the target's id, so blocks before it compare with the next lower float.
-// 60 registers: eight workgroups share a CU and keep its loads in flight.
+// 64 registers: eight workgroups share a CU and keep its loads in flight (with blocks
+// of twice the size and six workgroups the same rows take 3 to 5% longer).
 template <int DT>
 __global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int pieces, Piece* part, u64* part_keys) {
     constexpr int VE = DT == 2 ? 4 : 8;          // elements per vector
     constexpr int BLOCK = 64 * kVectors;         // vectors per block
-    constexpr int LIST = 256, FULL = 192;        // keys listed per wave; more are entered from memory
     __shared__ Piece waves[4];
-    __shared__ u64 lists[4][LIST];
+    __shared__ u64 lists[4][64];
+    __shared__ float quarters[4];                // the waves' ceil(K / 4)-th values so far
     const int r = blockIdx.x / pieces, piece = blockIdx.x - r * pieces;
     const int count = p.dev_count != nullptr ? min(p.max_rows, *p.dev_count) : p.max_rows;
     if (r >= count) return;
@@ -219,6 +278,13 @@ __global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int p
     const u32x4* body = reinterpret_cast<const u32x4*>(row + (int64_t)head * size);
     const int blocks = (vectors + BLOCK - 1) / BLOCK;
     const int b0 = (int)((int64_t)blocks * piece / pieces), b1 = (int)((int64_t)blocks * (piece + 1) / pieces);
+    u32x4 now[kVectors];
+    auto request = [&](int b) {
+#pragma unroll
+        for (int u = 0; u < kVectors; ++u)
+            now[u] = body[min(b * BLOCK + u * 64 + lane, vectors - 1)];
+    };
+    if (b0 + w < b1) request(b0 + w);            // under way while the target is looked up
     const int target = p.targets != nullptr ? p.targets[r] : -1;
     const bool has = target >= 0 && target < p.vocab;
     const float xt = has ? load_logit<DT>(row, target) : INFINITY;
@@ -230,44 +296,24 @@ __global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int p
     u64 best = 0;
     float floor_x = -INFINITY;                   // value of the K-th best key
     bool open = K > 0;                           // fewer than K keys yet
-    int listed = 0;
+    if (threadIdx.x < 4) quarters[threadIdx.x] = -INFINITY;
+    __syncthreads();
+    auto enter = [&](u64 key, u64 lanes) {       // the keys of these lanes
+        if (__popcll(lanes) > 12) {
+            best = join(best, sort64((lanes >> lane & 1) ? key : 0));
+        } else {
+            for (; lanes != 0; lanes &= lanes - 1) {
+                const u64 one = read_lane(key, __ffsll(lanes) - 1);
+                if (one > read_lane(best, K - 1)) insert(best, one);
+            }
+        }
+    };
     auto settle = [&]() {
         const u64 kth = read_lane(best, K - 1);
         open = kth == 0;
         floor_x = open ? -INFINITY : from_ordered((uint32_t)(kth >> 32));
-    };
-    auto enter = [&](u64 keys, u64 todo) {       // the lanes' keys, one after the other
-        for (; todo != 0; todo &= todo - 1) {
-            const u64 key = read_lane(keys, __ffsll(todo) - 1);
-            if (key > read_lane(best, K - 1)) insert(best, key);
-        }
-    };
-    auto list = [&](u64 key, bool maybe, u64 lanes) {
-        const int at = listed + __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
-        if (maybe) lists[w][at] = key;
-        listed += __popcll(lanes);
-    };
-    auto drain = [&]() {
-        __builtin_amdgcn_wave_barrier();
-        for (int at = 0; at < listed; at += 64) {
-            const int n = min(64, listed - at);
-            u64 keys = lane < n ? lists[w][at + lane] : 0;
-            if (n > 12) {
-#pragma unroll 1
-                for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll 1
-                    for (int o = k >> 1; o > 0; o >>= 1) {
-                        const u64 y = __shfl_xor(keys, o);
-                        keys = ((lane & o) == 0) == ((lane & k) == 0) ? max(keys, y) : min(keys, y);
-                    }
-                best = join(best, keys);
-            } else {
-                enter(keys, __ballot(lane < n));
-            }
-        }
-        listed = 0;
-        settle();
-        __builtin_amdgcn_wave_barrier();
+        const u64 quarter = read_lane(best, (K + 3) / 4 - 1);
+        if (lane == 0 && quarter != 0) *(volatile float*)&quarters[w] = from_ordered((uint32_t)(quarter >> 32));
     };
     auto weigh = [&](float x) {
         const float d = (x - (mine.m == -INFINITY ? 0.f : mine.m)) * kLog2e;
@@ -283,9 +329,12 @@ __global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int p
         mine.m = top;
     };
     auto wave_max = [&](float x) {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-        return x;
+        x = fmaxf(x, lane_xor<1>(x));
+        x = fmaxf(x, lane_xor<2>(x));
+        x = fmaxf(x, lane_xor<4>(x));
+        x = fmaxf(x, lane_xor<8>(x));
+        x = fmaxf(x, lane_xor<16>(x));
+        return fmaxf(x, lane_xor<32>(x));
     };
     auto loose = [&](int first, int n) {         // n < 8 single elements
         const bool in = lane < n;
@@ -294,15 +343,14 @@ __global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int p
         refer(wave_max(x));
         if (in) weigh(x);
         mine.above += __popcll(__ballot(in && has && (x > xt || (x == xt && id < target))));
-        if (K > 0) list(key_of(x, id), in, __ballot(in));
+        if (K > 0) {
+            enter(key_of(x, id), __ballot(in));
+            settle();
+        }
     };
 
     if (w == 0 && piece == 0 && head > 0) loose(0, head);
     for (int b = b0 + w; b < b1; b += 4) {
-        u32x4 now[kVectors];
-#pragma unroll
-        for (int u = 0; u < kVectors; ++u)
-            now[u] = __builtin_nontemporal_load(body + min(b * BLOCK + u * 64 + lane, vectors - 1));
         const bool whole_block = (b + 1) * BLOCK <= vectors;
         if (!whole_block) {                      // the row's last: lanes past its end see nothing
 #pragma unroll
@@ -341,67 +389,44 @@ __global__ __launch_bounds__(256, 8) void logprobs_kernel(LogprobParams p, int p
                 }
             }
         }
-        if (K > 0 && (open || __ballot(top > floor_x) != 0)) {
-            // Tokens of earlier blocks have lower ids: these must exceed their K-th.
-            float reach = open ? -INFINITY : floor_x;
-            const bool equal = open;
+        float shared_floor = -INFINITY;
+        if (K > 0) {
+            const volatile float* q = quarters;
+            shared_floor = fminf(fminf(q[0], q[1]), fminf(q[2], q[3]));
+        }
+        if (K > 0 && (open || __ballot(top > floor_x && top >= shared_floor) != 0)) {
+            // Tokens of the wave's earlier blocks have lower ids: these must exceed
+            // their K-th; of other waves' tokens nothing is known.
+            float reach = shared_floor;          // tokens >= reach pass
             if (open && whole_block) {
                 // 64 lanes' maxima, sorted: at least K tokens reach the K-th of them
-                float x = top;
-#pragma unroll 1
-                for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll 1
-                    for (int o = k >> 1; o > 0; o >>= 1) {
-                        const float y = __shfl_xor(x, o);
-                        x = ((lane & o) == 0) == ((lane & k) == 0) ? fmaxf(x, y) : fminf(x, y);
-                    }
-                reach = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), K - 1));
+                const float x = sort64(top);
+                reach = fmaxf(reach, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), K - 1)));
+            } else if (!open && floor_x >= reach) {
+                reach = higher_than(floor_x);
             }
-            // the lane's passing tokens, as bits; each is read again and listed
-            const bool all = equal && reach == -INFINITY;
-            const float over = equal ? lower_than(reach) : reach;
+            // the lane's passing tokens, as bits; each is read again and entered
             uint32_t passing = 0;
 #pragma unroll
             for (int u = 0; u < kVectors; ++u)
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    passing |= (all || element<DT>(now[u], e) > over) ? 1u << (u * VE + e) : 0u;
+                for (int e = 0; e < VE; ++e) passing |= element<DT>(now[u], e) >= reach ? 1u << (u * VE + e) : 0u;
             if (!whole_block) {
 #pragma unroll
                 for (int u = 0; u < kVectors; ++u)
                     if (b * BLOCK + u * 64 + lane >= vectors) passing &= ~(((1u << VE) - 1u) << (u * VE));
             }
-            bool many = false;
             for (u64 lanes = __ballot(passing != 0); lanes != 0; lanes = __ballot(passing != 0)) {
-                many = listed > FULL;
-                if (many) break;
                 const int k = __ffs(passing) - 1;
                 const int id = id0 + ((k / VE) * 64 + lane) * VE + k % VE;
-                const bool in = passing != 0;
-                list(key_of(in ? load_logit<DT>(row, id) : 0.f, id), in, lanes);
+                enter(passing != 0 ? key_of(load_logit<DT>(row, id), id) : 0, lanes);
                 passing &= passing - 1;
             }
-            if (many) {                          // more than the list takes (rising or equal tokens)
-                listed = 0;
-#pragma unroll 1
-                for (int k = lane; k < BLOCK * VE; k += 64) {
-                    const int id = id0 + k;
-                    const float x = id < head + vectors * VE ? load_logit<DT>(row, id) : -INFINITY;
-                    const u64 key = key_of(x, id);
-                    enter(key, __ballot(id < head + vectors * VE && key > read_lane(best, K - 1)));
-                }
-                if (b == b0 && w == 0 && piece == 0 && head > 0) {       // listed before the block
-                    const u64 key = lane < head ? key_of(load_logit<DT>(row, lane), lane) : 0;
-                    enter(key, __ballot(lane < head));
-                }
-                settle();
-            } else if (listed > 0) {
-                drain();
-            }
+            settle();
         }
+        if (b + 4 < b1) request(b + 4);
     }
     if (w == 0 && piece == pieces - 1 && tail > 0) loose(head + vectors * VE, tail);
-    if (listed > 0) drain();
 
     mine.S = wave_sum(mine.S);
     mine.W = wave_sum(mine.W);

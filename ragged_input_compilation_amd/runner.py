@@ -274,12 +274,18 @@ def _allocating_on(stream: int):
 
 
 def _attention(q, k_cache, scale=None, softcap=0.0, window=0, alibi_slopes=None, prefix_lens=None) -> ric.ric_attention:
-    if q.dtype not in (torch.float16, torch.bfloat16) or k_cache.dtype != q.dtype:
+    dtype = _DTYPE.get(q.dtype, ric.RIC_F32)
+    if dtype == ric.RIC_F32 or k_cache.dtype is not q.dtype:
         raise ValueError("q and the caches must be float16 or bfloat16, and alike")
-    return ric.make_attention(dtype=_DTYPE[q.dtype], num_heads=q.shape[1], num_kv_heads=k_cache.shape[2],
-                              head_dim=q.shape[2], block_size=k_cache.shape[1],
-                              scale=q.shape[2] ** -0.5 if scale is None else scale, softcap=softcap, window=window,
-                              alibi_slopes=_ptr(alibi_slopes), prefix_lens=_ptr(prefix_lens))
+    _, heads, dim = q.shape
+    _, block, kv_heads, _ = k_cache.shape
+    return ric.ric_attention(dtype, heads, kv_heads, dim, block, dim ** -0.5 if scale is None else scale, softcap, window,
+                             alibi_slopes.data_ptr() if alibi_slopes is not None else None,
+                             prefix_lens.data_ptr() if prefix_lens is not None else None)
+
+
+def _counts_ok(t: torch.Tensor, n: int) -> bool:
+    return t.dtype is torch.int32 and t.shape == (n,) and t.is_contiguous()
 
 
 def attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, num_reqs: int, max_query_len: int,
@@ -301,34 +307,36 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     int32; query_start_loc [num_reqs + 1], seq_lens [num_reqs] int32.  Without a
     workspace one is allocated where the call needs it."""
     a = _attention(q, k_cache, scale, softcap, window, alibi_slopes, prefix_lens)
+    tokens, heads, dim = shape = q.shape
     n = seq_lens.shape[0]
-    if k_cache.shape != v_cache.shape or v_cache.dtype != q.dtype or k_cache.shape[3] != q.shape[2]:
+    if k_cache.shape != v_cache.shape or v_cache.dtype is not q.dtype or k_cache.shape[3] != dim:
         raise ValueError("k_cache and v_cache must be [num_blocks, block_size, kv_heads, head_dim] of q's type")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous")
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("out must be like q")
-    for t in (q, out):
-        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-            raise ValueError("the heads of a token must be contiguous")
-    for t, k in ((query_start_loc, n + 1), (seq_lens, n), (prefix_lens, n)):
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != k or not t.is_contiguous()):
-            raise ValueError(f"query_start_loc [{n + 1}], seq_lens and prefix_lens [{n}] must be contiguous int32")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] < n or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    sq, so = q.stride(), out.stride()
+    if tokens and ((dim > 1 and (sq[2] != 1 or so[2] != 1)) or (heads > 1 and (sq[1] != dim or so[1] != dim))):
+        raise ValueError("the heads of a token must be contiguous")
+    if not (_counts_ok(query_start_loc, n + 1) and _counts_ok(seq_lens, n) and
+            (prefix_lens is None or _counts_ok(prefix_lens, n))):
+        raise ValueError(f"query_start_loc [{n + 1}], seq_lens and prefix_lens [{n}] must be contiguous int32")
+    rows, width = block_table.shape
+    st = block_table.stride()
+    if block_table.dtype is not torch.int32 or rows < n or (width > 1 and st[1] != 1):
         raise ValueError("block_table must be int32 [num_reqs, width] with contiguous rows")
-    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (q.shape[1],) or
+    if alibi_slopes is not None and (alibi_slopes.dtype is not torch.float32 or alibi_slopes.shape != (heads,) or
                                      not alibi_slopes.is_contiguous()):
         raise ValueError("alibi_slopes must be contiguous float32 [heads]")
     if workspace is None:
         workspace = attention_workspace(q, k_cache, n, max_query_len, max_seq_len)
-    ric.ric_paged_attention(a, _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_table),
-                            max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
-                            _ptr(query_start_loc), _ptr(seq_lens), n, q.shape[0], max_query_len, max_seq_len, _ptr(out),
-                            q_stride=q.stride(0) * 2 if q.shape[0] > 1 else 0,
-                            out_stride=out.stride(0) * 2 if out.shape[0] > 1 else 0, workspace=_ptr(workspace),
-                            workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size(),
-                            dev_status=dev_status, stream=current_stream())
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    many = tokens > 1
+    ric.ric_paged_attention(a, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
+                            block_table.data_ptr(), max(st[0], width), width, query_start_loc.data_ptr(),
+                            seq_lens.data_ptr(), n, tokens, max_query_len, max_seq_len, out.data_ptr(),
+                            sq[0] * 2 if many else 0, so[0] * 2 if many else 0, ws, ws_bytes, dev_status,
+                            current_stream())
     return out
 
 
@@ -407,12 +415,11 @@ def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor]):
     """Addresses of the layers' caches and the bytes of a page."""
     if not kc:
         return [], [], 0
-    n, dtype = kc[0].numel(), kc[0].dtype
-    for lst in (kc, vc):
-        for t in lst:
-            if not t.is_contiguous() or t.dtype is not dtype or t.numel() != n:
-                raise ValueError("the layers' caches must be contiguous and alike")
-    return [t.data_ptr() for t in kc], [t.data_ptr() for t in vc], n // kc[0].shape[0] * kc[0].element_size()
+    both = [*kc, *vc]
+    if len({t.numel() for t in both}) != 1 or len({t.dtype for t in both}) != 1 or \
+            not all([t.is_contiguous() for t in both]):
+        raise ValueError("the layers' caches must be contiguous and alike")
+    return [t.data_ptr() for t in kc], [t.data_ptr() for t in vc], kc[0][0].numel() * kc[0].element_size()
 
 
 def copy_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
