@@ -985,7 +985,7 @@ struct Plan {
     int dp;              // head size of the kernels
 };
 
-constexpr int kTargetGroups = 2048;      // workgroups that keep 256 CUs evenly busy
+constexpr int kTargetGroups = 1024;      // workgroups that keep 256 CUs evenly busy
 constexpr int kMinSplitLen = 256;
 
 Plan plan_of(const AttnParams& p) {
