@@ -737,41 +737,55 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
     const int p_wave_last = __builtin_amdgcn_readfirstlane(sp.seq - sp.n + min(rows - 1, row0 + w * 32 + 31) / G);
 
     // The wave loads a quarter of each tile: KT / 4 rows, RPL of them per load.
-    // Lane c looks up the page of row c of the quarter, one tile ahead, so that
-    // nothing but the next tile's address computation waits for it.
+    // Where pages hold whole quarters, a quarter's page id is a scalar, walked along
+    // without divisions and looked up a tile ahead, and the lanes' offsets are
+    // constants.  Other pages, and the tile in which the last key lies, are looked
+    // up lane by lane.
     constexpr int RPL = 1024 / (DP * 2), QROWS = KT / 4;
     auto block_of = [&](int j) { return p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size; };
-    auto key_of = [&](int j0) { return min(j0 + w * QROWS + (lane & (QROWS - 1)), key_end - 1); };
-    auto lookup = [&](int j0) { return table[min(block_of(key_of(j0)), p.table_width - 1)]; };
-    int piece_off[Shape::LOADS];                 // where in a row the lane's piece of load u starts
+    const __attribute__((address_space(4))) int32_t* entries = (const __attribute__((address_space(4))) int32_t*)table;
+    const bool paged = p.block_size % QROWS == 0 && p.table_width > 0;
+    uint32_t piece_off[Shape::LOADS];            // where in a row the lane's piece of load u starts
 #pragma unroll
     for (int u = 0; u < Shape::LOADS; ++u) {
         const int piece = (lane % CPR) ^ Shape::turn(w * QROWS + lane / CPR + RPL * u);
         piece_off[u] = EXACT || piece * 8 < dim ? piece * 16 : 0;
     }
-    const bool near = p.num_blocks * p.block_size * row_bytes < (int64_t(1) << 32);
-    auto load_tile = [&](int j0, int buf, int id) {
-        const int j = key_of(j0), blk = block_of(j);
-        const bool named = blk < p.table_width && (uint32_t)id < (uint64_t)p.num_blocks;
-        if (!named) *gap = 1;
-        const uint32_t slot = named ? id * p.block_size + (j - blk * p.block_size) : 0;
-        const uint32_t dst = lds0 + buf * 2 * TILE + w * Shape::LOADS * 1024;
-        if (near) {
-            const uint32_t start_of = slot * (uint32_t)row_bytes;
+    uint32_t lane_off[Shape::LOADS];             // and in a quarter
+#pragma unroll
+    for (int u = 0; u < Shape::LOADS; ++u) lane_off[u] = (lane / CPR + RPL * u) * (uint32_t)row_bytes + piece_off[u];
+    const int wu = __builtin_amdgcn_readfirstlane(w);
+    // the quarter that is loaded next: its block, first token there, page
+    int at_blk = block_of(key_begin + wu * QROWS), at_in = key_begin + wu * QROWS - at_blk * p.block_size, at_id = -1;
+    const int step_blk = block_of(KT), step_in = KT - step_blk * p.block_size;
+    auto look_up = [&]() { at_id = paged ? entries[min(at_blk, p.table_width - 1)] : -1; };
+    auto load_tile = [&](int j0, int buf) {
+        const uint32_t dst = lds0 + buf * 2 * TILE + wu * Shape::LOADS * 1024;
+        if (paged && j0 + KT <= key_end) {
+            const bool named = at_blk < p.table_width && (uint32_t)at_id < (uint64_t)p.num_blocks;
+            if (!named) *gap = 1;
+            const int64_t from = named ? ((int64_t)at_id * p.block_size + at_in) * row_bytes : 0;
 #pragma unroll
             for (int u = 0; u < Shape::LOADS; ++u) {
-                const uint32_t off = __shfl(start_of, lane / CPR + RPL * u) + piece_off[u];
-                load_to_lds(dst + u * 1024, kbase, off);
-                load_to_lds(dst + u * 1024 + TILE, vbase, off);
+                load_to_lds(dst + u * 1024, kbase + from, lane_off[u]);
+                load_to_lds(dst + u * 1024 + TILE, vbase + from, lane_off[u]);
             }
         } else {
 #pragma unroll
             for (int u = 0; u < Shape::LOADS; ++u) {
-                const int64_t off = (int64_t)__shfl(slot, lane / CPR + RPL * u) * row_bytes + piece_off[u];
-                load_to_lds(dst + u * 1024, kbase + off);
-                load_to_lds(dst + u * 1024 + TILE, vbase + off);
+                const int j = min(j0 + wu * QROWS + lane / CPR + RPL * u, key_end - 1), blk = block_of(j);
+                const int id = blk < p.table_width ? table[blk] : -1;
+                const bool named = (uint32_t)id < (uint64_t)p.num_blocks;
+                if (!named) *gap = 1;
+                const int64_t from = named ? ((int64_t)id * p.block_size + (j - blk * p.block_size)) * row_bytes + piece_off[u] : 0;
+                load_to_lds(dst + u * 1024, kbase + from);
+                load_to_lds(dst + u * 1024 + TILE, vbase + from);
             }
         }
+        at_in += step_in;
+        at_blk += step_blk + (at_in >= p.block_size ? 1 : 0);
+        at_in -= at_in >= p.block_size ? p.block_size : 0;
+        look_up();
     };
     // Where the lane's operands lie in a tile: K row c32 (+ 32 b), step k (+ 8); V^T
     // rows of its half and quarter (+ 16 k), columns d (+ 4).  Everything else
@@ -799,21 +813,15 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
 
     if (threadIdx.x == 0) *gap = 0;
     __syncthreads();
-    int next_id = -1;
-    if (ntiles > 0) {
-        load_tile(key_begin, 0, p.table_width > 0 ? lookup(key_begin) : -1);
-        if (p.table_width > 0) next_id = lookup(key_begin + KT);
-    }
+    look_up();
+    if (ntiles > 0) load_tile(key_begin, 0);
     auto step = [&](auto which, int t) __attribute__((always_inline)) {
         constexpr int BUF = decltype(which)::value, K0 = BUF * 2 * TILE, V0 = K0 + TILE;
         const int j0 = key_begin + t * KT;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         const bool gaps = *gap != 0;
-        if (t + 1 < ntiles) {
-            load_tile(j0 + KT, BUF ^ 1, next_id);
-            if (p.table_width > 0) next_id = lookup(j0 + 2 * KT);
-        }
+        if (t + 1 < ntiles) load_tile(j0 + KT, BUF ^ 1);
         if (j0 >= max(p_wave_last + 1, pre) || poisoned) return;      // nothing of the tile is seen by the wave's rows
         f32x16 s[KB];
 #pragma unroll
@@ -982,6 +990,7 @@ struct Plan {
     Cut cut;
     int nb;              // 16-row blocks of the few-rows part, 0: no such part
     bool chunks;         // some request may be larger
+    bool together;       // both parts in one launch
     int dp;              // head size of the kernels
 };
 
@@ -1004,11 +1013,15 @@ Plan plan_of(const AttnParams& p) {
     const int64_t keys = p.window > 0 && p.prefix == nullptr ? std::min<int64_t>(p.max_seq, (int64_t)p.window + p.max_q + 31) : p.max_seq;
     const int64_t groups = std::max<int64_t>(1, (int64_t)p.num_reqs * p.kv_heads);
     const int64_t want = std::max<int64_t>(1, kTargetGroups / groups);
+    // One launch for both parts where there may be enough single tokens to fill the
+    // card (124 requests of 8 K/V heads, 4 of them chunks: 755 us against 774 in two
+    // launches); two where there are few requests (4 chunks: 2070 us against 2260).
+    r.together = r.chunks && r.nb == 1 && groups >= 512;
     // Pieces of no more than 8192 keys, so that one long request does not outlast the
     // others; beside chunks 2048, as the two kinds' groups end together (mixed step
     // 755 us; pieces of 4096 831, of 1024 800).  256 requests of up to 4096 keys take
     // 434 us uncut, 528 in pieces of 2048 and 562 in pieces of 1024.
-    const int64_t longest = r.chunks ? 2048 : 8192;
+    const int64_t longest = r.together ? 2048 : 8192;
     c.min_len = (int)std::min<int64_t>(longest, std::max<int64_t>(kMinSplitLen, ((keys + want - 1) / want + 31) / 32 * 32));
     c.splits = (int)std::max<int64_t>(1, std::min<int64_t>((keys + c.min_len - 1) / c.min_len, std::min<int64_t>(std::max<int64_t>(want, 16), 256)));
     c.row_groups = r.nb > 0 ? p.num_reqs * c.splits * p.kv_heads : 0;
@@ -1025,7 +1038,7 @@ void launch(const AttnParams& p, const Plan& r, Partial part, hipStream_t s) {
     const Cut& c = r.cut;
     // caps, biases and a scale of zero need the whole score before the mask
     const bool feat = p.cap > 0.f || p.slopes != nullptr || p.scale == 0.f;
-    if (r.chunks && r.nb == 1) {
+    if (r.together) {
         const dim3 grid(((c.tile_groups + 7) / 8 + (c.row_groups + 7) / 8) * 8);
         if (feat) hipLaunchKernelGGL((attention_mixed_kernel<DP, BF16, EXACT, true>), grid, dim3(256), 0, s, p, part, c);
         else hipLaunchKernelGGL((attention_mixed_kernel<DP, BF16, EXACT, false>), grid, dim3(256), 0, s, p, part, c);
