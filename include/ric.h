@@ -492,7 +492,8 @@ typedef struct {
     int32_t block_size;           /* tokens per cache page                                        */
     float scale;                  /* scores are scale * q.k                                       */
     float softcap;                /* c > 0: scores become c * tanh(score / c); 0: no cap          */
-    int32_t window;               /* w > 0: position p sees only keys j > p - w; 0: no window     */
+    int32_t window;               /* w > 0: position p sees only keys j > p - w (w <= 2^30); 0: no
+                                     window                                                       */
     const float* alibi_slopes;    /* DEVICE float[num_heads]: slope * |p - j| is subtracted from
                                      the (capped) score; NULL: no bias                            */
     const int32_t* prefix_lens;   /* DEVICE int32[num_reqs]: request i's keys j < prefix_lens[i]
@@ -531,8 +532,8 @@ typedef struct {
  *   max_seq_len  longest request expected; only the way the work is split goes
  *                by it (a longer one is still right)
  *   workspace    DEVICE, ric_paged_attention_workspace_bytes() of the same
- *                arguments (may be 0: then NULL), 16-byte aligned, contents
- *                undefined after the call.  Calls that may run at the same time
+ *                arguments (may be 0: then NULL; the window, prefix, cap and bias do
+ *                not change it), 16-byte aligned, contents undefined after the call.  Calls that may run at the same time
  *                (two streams, two graphs) need one each
  * Everything is read on the device, so a captured call replays with new counts
  * as long as num_reqs, num_tokens and max_query_len still bound them.  Runs on the

@@ -992,6 +992,7 @@ struct Plan {
     bool chunks;         // some request may be larger
     bool together;       // both parts in one launch
     int dp;              // head size of the kernels
+    int most_splits;     // bound of cut.splits for any window and prefix (workspaces go by it)
 };
 
 constexpr int kTargetGroups = 1024;      // workgroups that keep 256 CUs evenly busy
@@ -1000,7 +1001,7 @@ constexpr int kMinSplitLen = 256;
 Plan plan_of(const AttnParams& p) {
     Plan r{};
     const int G = p.heads / p.kv_heads;
-    const int64_t most = (int64_t)p.max_q * G;
+    const int64_t most = (int64_t)std::max(p.max_q, 1) * G;
     r.dp = p.dim <= 64 ? 64 : p.dim <= 128 ? 128 : 256;
     // Requests of up to 64 rows per K/V head take the few-rows kernel; beside
     // larger ones, those of a single token do.
@@ -1024,6 +1025,11 @@ Plan plan_of(const AttnParams& p) {
     const int64_t longest = r.together ? 2048 : 8192;
     c.min_len = (int)std::min<int64_t>(longest, std::max<int64_t>(kMinSplitLen, ((keys + want - 1) / want + 31) / 32 * 32));
     c.splits = (int)std::max<int64_t>(1, std::min<int64_t>((keys + c.min_len - 1) / c.min_len, std::min<int64_t>(std::max<int64_t>(want, 16), 256)));
+    // fewer keys (a window) are cut into at most `want` pieces of at least kMinSplitLen
+    const int64_t all = std::max<int64_t>(p.max_seq, 1);
+    r.most_splits = (int)std::max<int64_t>({c.splits, std::min(want, (all + kMinSplitLen - 1) / kMinSplitLen),
+                                            std::min<int64_t>((all + longest - 1) / longest, std::max<int64_t>(want, 16))});
+    r.most_splits = std::min(r.most_splits, 256);
     c.row_groups = r.nb > 0 ? p.num_reqs * c.splits * p.kv_heads : 0;
     c.tile_groups = r.chunks ? (int)(((int64_t)p.num_tokens * G / kRowTile + p.num_reqs) * p.kv_heads) : 0;
     return r;
@@ -1057,7 +1063,8 @@ void launch(const AttnParams& p, const Plan& r, Partial part, hipStream_t s) {
 
 size_t attention_workspace(const AttnParams& p) {
     const Plan r = plan_of(p);
-    return (size_t)partial_rows(p, r) * (r.dp * 4 + 8);
+    if (r.nb == 0 || r.most_splits <= 1) return 0;
+    return (size_t)p.num_reqs * p.kv_heads * r.cut.max_rows * r.most_splits * (r.dp * 4 + 8);
 }
 
 hipError_t launch_attention(const AttnParams& p, void* workspace, hipStream_t s) {

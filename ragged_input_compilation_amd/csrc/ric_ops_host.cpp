@@ -34,7 +34,7 @@ int check_attention(const ric_attention* a, int32_t num_reqs, int32_t num_tokens
     if (a->block_size < 1) return fail(RIC_EINVAL, "block_size %d < 1", a->block_size);
     if (!std::isfinite(a->scale)) return fail(RIC_EINVAL, "scale is not finite");
     if (!(a->softcap >= 0.f) || !std::isfinite(a->softcap)) return fail(RIC_EINVAL, "softcap must be finite and >= 0");
-    if (a->window < 0) return fail(RIC_EINVAL, "window %d < 0", a->window);
+    if (a->window < 0 || a->window > (1 << 30)) return fail(RIC_EINVAL, "window %d outside [0, 2^30]", a->window);
     if (num_reqs < 0 || num_tokens < 0) return fail(RIC_EINVAL, "negative count");
     if (num_tokens > kMaxOperatorRows) return fail(RIC_EINVAL, "num_tokens %d above %d per call", num_tokens, kMaxOperatorRows);
     // Grids stay below 2^24 workgroups of 256 lanes: a request's rows are cut into
@@ -80,11 +80,15 @@ int check_pages(ric_batch* b, int32_t group, int32_t n, const int32_t* src, cons
     if (rc) return rc;
     rc = check_blocks(b, group, dst, n);
     if (rc) return rc;
-    std::unordered_set<int32_t> sources(src, src + n), dests;
-    if (distinct_src && (int32_t)sources.size() != n) return fail(RIC_EINVAL, "a page is listed twice as a source");
-    for (int32_t k = 0; k < n; ++k) {
-        if (!dests.insert(dst[k]).second) return fail(RIC_EINVAL, "page %d is listed twice as a destination", dst[k]);
-        if (sources.count(dst[k])) return fail(RIC_EINVAL, "page %d is both a source and a destination", dst[k]);
+    try {
+        std::unordered_set<int32_t> sources(src, src + n), dests;
+        if (distinct_src && (int32_t)sources.size() != n) return fail(RIC_EINVAL, "a page is listed twice as a source");
+        for (int32_t k = 0; k < n; ++k) {
+            if (!dests.insert(dst[k]).second) return fail(RIC_EINVAL, "page %d is listed twice as a destination", dst[k]);
+            if (sources.count(dst[k])) return fail(RIC_EINVAL, "page %d is both a source and a destination", dst[k]);
+        }
+    } catch (const std::bad_alloc&) {
+        return fail(RIC_ENOMEM, "host allocation failed");
     }
     return RIC_OK;
 }
@@ -94,7 +98,12 @@ int copy_pages(ric_batch* b, int32_t group, int32_t n, const int32_t* src, const
     if (n == 0) return RIC_OK;
     int rc = refuse_if_capturing(b);
     if (rc) return rc;
-    std::vector<std::pair<int32_t, int32_t>> pairs((size_t)n);
+    std::vector<std::pair<int32_t, int32_t>> pairs;
+    try {
+        pairs.resize((size_t)n);
+    } catch (const std::bad_alloc&) {
+        return fail(RIC_ENOMEM, "host allocation failed");
+    }
     for (int32_t k = 0; k < n; ++k) pairs[k] = {src[k], dst[k]};
     if (tables) std::sort(pairs.begin(), pairs.end());
     // A 16-KiB piece of a page is one workgroup: fewer pairs per launch for

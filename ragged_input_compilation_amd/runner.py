@@ -284,6 +284,13 @@ def _attention(q, k_cache, scale=None, softcap=0.0, window=0, alibi_slopes=None,
                              prefix_lens.data_ptr() if prefix_lens is not None else None)
 
 
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must lie on the current device (cuda:{dev})")
+
+
 def _counts_ok(t: torch.Tensor, n: int) -> bool:
     return t.dtype is torch.int32 and t.shape == (n,) and t.is_contiguous()
 
@@ -328,6 +335,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if alibi_slopes is not None and (alibi_slopes.dtype is not torch.float32 or alibi_slopes.shape != (heads,) or
                                      not alibi_slopes.is_contiguous()):
         raise ValueError("alibi_slopes must be contiguous float32 [heads]")
+    _on_current_device(q, k_cache, v_cache, block_table, query_start_loc, seq_lens, out, alibi_slopes, prefix_lens, workspace)
     if workspace is None:
         workspace = attention_workspace(q, k_cache, n, max_query_len, max_seq_len)
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -354,15 +362,27 @@ def step_attention(batch: "Batch", step: ric.ric_step, q: torch.Tensor, k_cache:
     if k_cache.shape != v_cache.shape or v_cache.dtype != q.dtype or k_cache.shape[3] != q.shape[2] or \
             not (k_cache.is_contiguous() and v_cache.is_contiguous() and q.is_contiguous() and out.is_contiguous()):
         raise ValueError("contiguous q, out and caches of one type are needed")
-    if workspace is None:
-        with _allocating_on(batch.stream):
-            workspace = attention_workspace(q, k_cache, step.num_reqs, step.max_query_len, step.max_seq_len)
-    ric.ric_paged_attention(a, _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], cols.group_blocks[group],
-                            cols.group_block_stride[group], cols.group_block_stride[group], step.query_start_loc,
-                            step.seq_lens, step.num_reqs, q.shape[0], step.max_query_len, step.max_seq_len, _ptr(out),
-                            workspace=_ptr(workspace),
-                            workspace_bytes=0 if workspace is None else workspace.numel(), dev_status=dev_status,
-                            stream=batch.stream)
+    cfg = batch.cfg
+    if k_cache.shape[1] != (cfg.block_size if group == 0 else cfg.group_block_size[group]):
+        raise ValueError("the caches' block size is not the group's")
+    prefix, slopes = kw.get("prefix_lens"), kw.get("alibi_slopes")
+    if (prefix is not None and not _counts_ok(prefix, step.num_reqs)) or \
+            (slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (q.shape[1],) or
+                                     not slopes.is_contiguous())):
+        raise ValueError("prefix_lens must be contiguous int32 [num_reqs], alibi_slopes contiguous float32 [heads]")
+    dev = batch.workspace.get_device()
+    if any(t is not None and t.get_device() != dev for t in (q, out, k_cache, v_cache, workspace, prefix, slopes)):
+        raise ValueError("every tensor must lie on the batch's device")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            with _allocating_on(batch.stream):
+                workspace = attention_workspace(q, k_cache, step.num_reqs, step.max_query_len, step.max_seq_len)
+        ric.ric_paged_attention(a, _ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], cols.group_blocks[group] or 0,
+                                cols.group_block_stride[group], cols.group_block_stride[group], step.query_start_loc,
+                                step.seq_lens, step.num_reqs, q.shape[0], step.max_query_len, step.max_seq_len,
+                                _ptr(out), workspace=_ptr(workspace),
+                                workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                dev_status=dev_status, stream=batch.stream)
     return out
 
 
@@ -401,6 +421,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top_k:
     elif out.logprob.shape[0] < rows or out.top_ids.shape[1] != top_k:
         raise ValueError("out is too small, or of another top_k")
     has = targets is not None
+    _on_current_device(logits, targets, out.logprob, out.rank, out.entropy, out.top_ids, out.top_logprobs, out.workspace)
     ric.ric_token_logprobs(_ptr(logits), _DTYPE[logits.dtype], _ptr(targets), rows, vocab, top_k,
                            _ptr(out.logprob) if has else 0, _ptr(out.rank) if has else 0, _ptr(out.entropy),
                            _ptr(out.top_ids) if top_k else 0, _ptr(out.top_logprobs) if top_k else 0,
@@ -411,26 +432,27 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top_k:
     return out
 
 
-def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor]):
+def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor], device: int):
     """Addresses of the layers' caches and the bytes of a page."""
     if not kc:
         return [], [], 0
     both = [*kc, *vc]
     if len({t.numel() for t in both}) != 1 or len({t.dtype for t in both}) != 1 or \
+            {t.get_device() for t in both} != {device} or \
             not all([t.is_contiguous() for t in both]):
-        raise ValueError("the layers' caches must be contiguous and alike")
+        raise ValueError("the layers' caches must be contiguous, alike and on the batch's device")
     return [t.data_ptr() for t in kc], [t.data_ptr() for t in vc], kc[0][0].numel() * kc[0].element_size()
 
 
 def copy_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
     """Page src[k] -> page dst[k] in every layer's caches [num_blocks, ...] (ric_copy_blocks)."""
-    k, v, n = _pages(kc, vc)
+    k, v, n = _pages(kc, vc, batch.workspace.get_device())
     ric.ric_copy_blocks(batch.h, src, dst, k, v, n, group)
 
 
 def move_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
     """copy_blocks, and the live requests' block tables follow (ric_move_blocks)."""
-    k, v, n = _pages(kc, vc)
+    k, v, n = _pages(kc, vc, batch.workspace.get_device())
     ric.ric_move_blocks(batch.h, src, dst, k, v, n, group)
 
 
@@ -448,6 +470,6 @@ def block_refs(batch: "Batch", group: int = 0) -> torch.Tensor:
 def fork_request(batch: "Batch", parent_id: int, child_id: int, num_tokens: int, num_computed: int, new_blocks,
                  kc: List[torch.Tensor], vc: List[torch.Tensor], sampling=None) -> int:
     """A new request over the parent's history, sharing its full pages (ric_fork_request)."""
-    k, v, n = _pages(kc, vc)
+    k, v, n = _pages(kc, vc, batch.workspace.get_device())
     return ric.ric_fork_request(batch.h, parent_id, child_id, num_tokens, num_computed, new_blocks, k, v,
                                 n // batch.cfg.block_size, sampling)

@@ -155,6 +155,45 @@ def test_a_request_longer_than_declared_is_left_alone(runner):
             check_attention(got[rows], want[rows], tol[rows])
 
 
+def test_no_query_length_declared(runner):
+    inp = attention_inputs([(1, 30), (1, 5)], heads=4, kv_heads=1, dim=64, block=16, dtype=torch.float16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = call(runner, inp, scale=0.1, status=status, max_q=0)
+    assert (got == 77.0).all() and status.item() > 0
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, torch.float16), (128, torch.bfloat16), (40, torch.bfloat16), (256, torch.float16)])
+@pytest.mark.parametrize("kw", [dict(), dict(window=70), dict(softcap=10.0, slopes=[0.05] * 16), dict(scale=-0.2),
+                                dict(scale=0.0, prefix="half")],
+                         ids=["plain", "window", "cap-bias", "negative-scale", "zero-scale-prefix"])
+def test_many_requests_of_both_kinds(runner, dim, dtype, kw):
+    """Enough single tokens beside chunks for the launch that holds both."""
+    reqs = [(1, 1 + (37 * k) % 400) for k in range(40)] + [(150, 300), (33, 33)] + [(1, 900), (2, 2500), (1, 64)] * 10
+    kw = dict(kw)
+    kw.setdefault("scale", dim ** -0.5)
+    if kw.get("prefix") == "half":
+        kw["prefix"] = [t // 2 for _, t in reqs]
+    inp = attention_inputs(reqs, heads=16, kv_heads=8, dim=dim, block=16, dtype=dtype, seed=21, pad_tokens=2)
+    both(runner, inp, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_keys_behind_the_mask_never_arrive(runner, dim):
+    """NaN and infinite K rows that only later rows of a chunk see."""
+    reqs = [(40, 40), (130, 300), (5, 64)]
+    inp = attention_inputs(reqs, heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=6)
+    for i, j, value in ((0, 17, float("nan")), (1, 290, float("inf")), (2, 61, float("nan"))):
+        inp["kc"][inp["table"][i, j // 16].long(), j % 16, :, 3] = value
+    got = call(runner, inp, scale=dim ** -0.5).float()
+    want, tol = attention_reference(inp, scale=dim ** -0.5)
+    start = 0
+    for (n, t), j in zip(reqs, (17, 290, 61)):
+        first = j - (t - n)                     # the first row that sees the key
+        check_attention(got[start:start + first], want[start:start + first], tol[start:start + first])
+        start += n
+    assert torch.isnan(got[17:40]).all() and torch.isnan(got[170 + 2:170 + 5]).all()
+
+
 @pytest.mark.parametrize("dim", [64, 128, 48])
 def test_strided_rows_in_place_and_a_wider_table(runner, dim):
     reqs = CHUNKS + SPEC

@@ -40,7 +40,8 @@ def test_attention_refusals(ric):
     for kw in (dict(dtype=ric.RIC_F32), dict(dtype=7), dict(num_heads=0), dict(num_kv_heads=0), dict(num_heads=9),
                dict(num_heads=70000, num_kv_heads=70000), dict(head_dim=0), dict(head_dim=12), dict(head_dim=264),
                dict(block_size=0), dict(scale=float("nan")), dict(scale=float("inf")), dict(softcap=-1.0),
-               dict(softcap=float("nan")), dict(softcap=float("inf")), dict(window=-1)):
+               dict(softcap=float("nan")), dict(softcap=float("inf")), dict(window=-1), dict(window=(1 << 30) + 1),
+               dict(num_heads=520, num_kv_heads=4)):
         a = _attention(ric, **kw)
         assert code(ric, ric.ric_paged_attention, a, **CALL) == ric.RIC_EINVAL, kw
         assert ric.ric_paged_attention_workspace_bytes(a, 2, 2, 1, 20) == 0
@@ -60,6 +61,20 @@ def test_attention_refusals(ric):
         long = {**CALL, "num_reqs": 1, "num_tokens": 1, "max_seq_len": 100000}
         for ws in (dict(), dict(workspace=4096, workspace_bytes=need - 256 - 1), dict(workspace=4104, workspace_bytes=need)):
             assert code(ric, ric.ric_paged_attention, a, **{**long, **ws}) == ric.RIC_EINVAL, ws
+
+
+def test_attention_workspace_does_not_depend_on_the_mask(ric):
+    """One workspace serves the layers of a model with and without windows."""
+    rng = np.random.default_rng(1)
+    for _ in range(400):
+        reqs, q = int(rng.integers(1, 300)), int(rng.integers(1, 70))
+        kv = int(rng.choice([1, 2, 8]))
+        args = (reqs, reqs * q, q, int(np.exp(rng.uniform(0, 13))))
+        kw = dict(num_kv_heads=kv, num_heads=kv * int(rng.choice([1, 4, 8])), head_dim=int(rng.choice([64, 128, 80])))
+        base = ric.ric_paged_attention_workspace_bytes(_attention(ric, **kw), *args)
+        for w in (1, 500, 1024, 5000, 32768, 1 << 30):
+            assert ric.ric_paged_attention_workspace_bytes(_attention(ric, window=w, **kw), *args) == base
+        assert base < 1 << 30
 
 
 def test_logprobs_refusals(ric):
