@@ -31,7 +31,8 @@
  *   - A handle belongs to the device that was current at ric_create; calls on
  *     it make that device current for their duration and restore the
  *     caller's.  Calls without a handle (ric_reshape_and_cache,
- *     ric_gather_rows) run on the current device, whose stream they take.
+ *     ric_gather_rows, ric_paged_attention, ric_token_logprobs) run on the
+ *     current device, whose stream they take.
  *   - A handle is not thread-safe: one thread at a time per handle.
  */
 #ifndef RIC_H
@@ -521,8 +522,8 @@ typedef struct {
  *                contiguous (the layout ric_reshape_and_cache writes)
  *   block_table  DEVICE int32: row i at block_table + i * block_table_stride, its
  *                first block_table_width entries readable.  A key whose page id
- *                lies outside [0, num_blocks), or past the table's width, is left
- *                out of its row; *dev_status (optional) is then raised.  Ids of
+ *                lies outside [0, num_blocks), or past the table's width, or at
+ *                2^30 or later, is left out of its row; *dev_status (optional) is then raised.  Ids of
  *                invisible keys are not looked at
  *   query_start_loc, seq_lens  DEVICE int32[num_reqs + 1], [num_reqs]
  *                (ric_step's arrays).  Rows of out outside every request
@@ -533,12 +534,13 @@ typedef struct {
  *                by it (a longer one is still right)
  *   workspace    DEVICE, ric_paged_attention_workspace_bytes() of the same
  *                arguments (may be 0: then NULL; the window, prefix, cap and bias do
- *                not change it), 16-byte aligned, contents undefined after the call.  Calls that may run at the same time
- *                (two streams, two graphs) need one each
+ *                not change it), 16-byte aligned, contents undefined after the call.  Calls
+ *                that may run at the same time (two streams, two graphs) need one
+ *                each
  * Everything is read on the device, so a captured call replays with new counts
  * as long as num_reqs, num_tokens and max_query_len still bound them.  Runs on the
- * current device.  num_tokens <= 2^22, num_reqs <= 65535.  Equal inputs give equal bits.  Errors:
- * EINVAL (shapes, strides, alignment, NULL, workspace too small), EHIP. */
+ * current device.  num_tokens <= 2^22, num_reqs <= 65535, num_tokens * num_heads < 2^31.
+ * Equal inputs give equal bits.  Errors: EINVAL (shapes, strides, alignment, NULL, workspace too small), EHIP. */
 size_t ric_paged_attention_workspace_bytes(const ric_attention* a, int32_t num_reqs, int32_t num_tokens,
                                            int32_t max_query_len, int32_t max_seq_len);  /* 0 also on EINVAL */
 int ric_paged_attention(const ric_attention* a, const void* q, int64_t q_stride, const void* k_cache,
@@ -572,9 +574,10 @@ int ric_paged_attention(const ric_attention* a, const void* q, int64_t q_stride,
  *   logprob, rank, entropy  DEVICE float / int32 / float [max_rows]; entropy may
  *                be NULL
  *   top_ids, top_logprobs  DEVICE int32 / float [max_rows][top_k]
- *   workspace    DEVICE, ric_token_logprobs_workspace_bytes() bytes (may be 0),
+ *   workspace    DEVICE, ric_token_logprobs_workspace_bytes() bytes (may be 0;
+ *                enough for calls of fewer rows, tokens or alternatives as well),
  *                16-byte aligned; one per call that may run at the same time
- * Runs on the current device.  max_rows <= 2^22.  Equal inputs give equal bits.
+ * Runs on the current device.  max_rows <= 2^22, vocab <= 2^30.  Equal inputs give equal bits.
  * Errors: EINVAL, EHIP. */
 #define RIC_MAX_TOP_LOGPROBS 64
 size_t ric_token_logprobs_workspace_bytes(int32_t max_rows, int32_t vocab, int32_t top_k);

@@ -256,6 +256,7 @@ hipError_t launch_fork(const ForkParams& p, bool rows, hipStream_t s);
 size_t attention_workspace(const AttnParams& p);
 hipError_t launch_attention(const AttnParams& p, void* workspace, hipStream_t s);
 size_t logprobs_workspace(int32_t max_rows, int32_t vocab, int32_t top_k);
+size_t logprobs_workspace_up_to(int32_t max_rows, int32_t vocab, int32_t top_k);   // of any fewer rows, too
 hipError_t launch_logprobs(const LogprobParams& p, void* workspace, hipStream_t s);
 
 // Compile plus the K/V write of `num_layers` (<= kMaxLayersPerLaunch) layers

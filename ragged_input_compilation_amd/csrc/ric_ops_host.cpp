@@ -21,6 +21,7 @@ using namespace ric;
 namespace {
 
 constexpr int32_t kMaxOperatorRows = 1 << 22;   // tokens or logits rows per call
+constexpr int32_t kMaxVocab = 1 << 30;          // token ids and the strides over them stay below 2^31
 
 int check_attention(const ric_attention* a, int32_t num_reqs, int32_t num_tokens, int32_t max_query_len,
                     int32_t max_seq_len, AttnParams* p) {
@@ -196,8 +197,9 @@ int ric_paged_attention(const ric_attention* a, const void* q, int64_t q_stride,
 }
 
 size_t ric_token_logprobs_workspace_bytes(int32_t max_rows, int32_t vocab, int32_t top_k) {
-    if (max_rows <= 0 || max_rows > kMaxOperatorRows || vocab < 1 || top_k < 0 || top_k > kMaxTopLogprobs) return 0;
-    return align_up(logprobs_workspace(max_rows, vocab, top_k), kAlign);
+    if (max_rows <= 0 || max_rows > kMaxOperatorRows || vocab < 1 || vocab > kMaxVocab || top_k < 0 || top_k > kMaxTopLogprobs)
+        return 0;
+    return align_up(logprobs_workspace_up_to(max_rows, vocab, top_k), kAlign);
 }
 
 int ric_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* targets,
@@ -207,7 +209,7 @@ int ric_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, co
     if (dtype != RIC_F16 && dtype != RIC_BF16 && dtype != RIC_F32) return fail(RIC_EINVAL, "unknown dtype %d", dtype);
     if (max_rows < 0 || max_rows > kMaxOperatorRows)
         return fail(RIC_EINVAL, "max_rows %d outside [0, %d]", max_rows, kMaxOperatorRows);
-    if (vocab < 1) return fail(RIC_EINVAL, "vocab %d < 1", vocab);
+    if (vocab < 1 || vocab > kMaxVocab) return fail(RIC_EINVAL, "vocab %d outside [1, 2^30]", vocab);
     if (top_k < 0 || top_k > kMaxTopLogprobs || top_k > vocab)
         return fail(RIC_EINVAL, "top_k %d outside [0, min(%d, vocab)]", top_k, kMaxTopLogprobs);
     const int64_t size = dtype == RIC_F32 ? 4 : 2;

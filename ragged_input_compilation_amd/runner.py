@@ -297,8 +297,9 @@ def _counts_ok(t: torch.Tensor, n: int) -> bool:
 
 def attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, num_reqs: int, max_query_len: int,
                         max_seq_len: int) -> Optional[torch.Tensor]:
-    """A workspace for paged_attention calls of these bounds (None: none needed).
-    Calls that may run at the same time need one each."""
+    """A workspace for paged_attention calls with these counts and bounds (None:
+    none needed).  Fewer requests may be cut further and need more.  Calls that
+    may run at the same time need one each."""
     n = ric.ric_paged_attention_workspace_bytes(_attention(q, k_cache), num_reqs, q.shape[0], max_query_len, max_seq_len)
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
@@ -325,13 +326,15 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     sq, so = q.stride(), out.stride()
     if tokens and ((dim > 1 and (sq[2] != 1 or so[2] != 1)) or (heads > 1 and (sq[1] != dim or so[1] != dim))):
         raise ValueError("the heads of a token must be contiguous")
+    if tokens > 1 and (sq[0] < heads * dim or so[0] < heads * dim):
+        raise ValueError("the tokens of q and out must not overlap")
     if not (_counts_ok(query_start_loc, n + 1) and _counts_ok(seq_lens, n) and
             (prefix_lens is None or _counts_ok(prefix_lens, n))):
         raise ValueError(f"query_start_loc [{n + 1}], seq_lens and prefix_lens [{n}] must be contiguous int32")
     rows, width = block_table.shape
     st = block_table.stride()
-    if block_table.dtype is not torch.int32 or rows < n or (width > 1 and st[1] != 1):
-        raise ValueError("block_table must be int32 [num_reqs, width] with contiguous rows")
+    if block_table.dtype is not torch.int32 or rows < n or (width > 1 and st[1] != 1) or (rows > 1 and st[0] < width):
+        raise ValueError("block_table must be int32 [num_reqs, width] with contiguous rows of their own")
     if alibi_slopes is not None and (alibi_slopes.dtype is not torch.float32 or alibi_slopes.shape != (heads,) or
                                      not alibi_slopes.is_contiguous()):
         raise ValueError("alibi_slopes must be contiguous float32 [heads]")
@@ -356,6 +359,7 @@ def step_attention(batch: "Batch", step: ric.ric_step, q: torch.Tensor, k_cache:
     own query_start_loc, seq_lens and block table.  Enqueued on the handle's
     stream; ``kw``: scale, softcap, window, alibi_slopes, prefix_lens."""
     a = _attention(q, k_cache, **kw)
+    _pool(batch, group)                             # a group the handle may have
     cols = ric.ric_get_columns(batch.h)
     if q.shape[0] != step.num_tokens_padded or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("q and out must hold the step's padded tokens")
@@ -398,7 +402,8 @@ class Logprobs:
 
 
 def alloc_logprobs(rows: int, vocab: int, top_k: int, device="cuda") -> Logprobs:
-    """Output and workspace tensors for token_logprobs calls of up to ``rows`` rows."""
+    """Output and workspace tensors for token_logprobs calls of up to ``rows`` rows
+    of up to ``vocab`` logits."""
     f = lambda *s: torch.empty(s, dtype=torch.float32, device=device)
     i = lambda *s: torch.empty(s, dtype=torch.int32, device=device)
     n = ric.ric_token_logprobs_workspace_bytes(rows, vocab, top_k)
@@ -414,6 +419,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top_k:
     if logits.dim() != 2 or logits.dtype not in _DTYPE or (logits.numel() and logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be [rows, vocab] of float16, bfloat16 or float32 with contiguous rows")
     rows, vocab = logits.shape
+    if rows > 1 and logits.stride(0) < vocab:
+        raise ValueError("the rows of logits must not overlap")
     if targets is not None and (targets.dtype != torch.int32 or targets.shape != (rows,) or not targets.is_contiguous()):
         raise ValueError("targets must be contiguous int32 [rows]")
     if out is None:
@@ -432,11 +439,26 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor], top_k:
     return out
 
 
-def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor], device: int):
-    """Addresses of the layers' caches and the bytes of a page."""
+def _pool(batch: "Batch", group: int) -> int:
+    """Pages of the group's pool."""
+    c = batch.cfg
+    if not 0 <= group < max(1, c.num_kv_groups):
+        raise ValueError(f"group {group} outside [0, {max(1, c.num_kv_groups)})")
+    return c.num_kv_blocks if group == 0 or c.group_num_kv_blocks[group] <= 0 else c.group_num_kv_blocks[group]
+
+
+def _pages(batch: "Batch", kc: List[torch.Tensor], vc: List[torch.Tensor], group: int, *named):
+    """Addresses of the layers' caches and the bytes of a page; ``named``: lists of
+    the pages that the call is given."""
+    if len(kc) != len(vc):
+        raise ValueError("kc and vc must hold one cache per layer each")
     if not kc:
         return [], [], 0
+    device = batch.workspace.get_device()
     both = [*kc, *vc]
+    pages = kc[0].shape[0]                          # ids are checked against the group's pool by the call
+    if pages < _pool(batch, group) and any(len(ids) and np.max(ids) >= pages for ids in named):
+        raise ValueError("a page lies past the caches' end")
     if len({t.numel() for t in both}) != 1 or len({t.dtype for t in both}) != 1 or \
             {t.get_device() for t in both} != {device} or \
             not all([t.is_contiguous() for t in both]):
@@ -446,21 +468,20 @@ def _pages(kc: List[torch.Tensor], vc: List[torch.Tensor], device: int):
 
 def copy_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
     """Page src[k] -> page dst[k] in every layer's caches [num_blocks, ...] (ric_copy_blocks)."""
-    k, v, n = _pages(kc, vc, batch.workspace.get_device())
+    k, v, n = _pages(batch, kc, vc, group, src, dst)
     ric.ric_copy_blocks(batch.h, src, dst, k, v, n, group)
 
 
 def move_blocks(batch: "Batch", src, dst, kc: List[torch.Tensor], vc: List[torch.Tensor], group: int = 0) -> None:
     """copy_blocks, and the live requests' block tables follow (ric_move_blocks)."""
-    k, v, n = _pages(kc, vc, batch.workspace.get_device())
+    k, v, n = _pages(batch, kc, vc, group, src, dst)
     ric.ric_move_blocks(batch.h, src, dst, k, v, n, group)
 
 
 def block_refs(batch: "Batch", group: int = 0) -> torch.Tensor:
     """Table entries that name each page of the group's pool, int32 (ric_block_refs),
     written on the handle's stream."""
-    c = batch.cfg
-    pool = c.num_kv_blocks if group == 0 or c.group_num_kv_blocks[group] <= 0 else c.group_num_kv_blocks[group]
+    pool = _pool(batch, group)
     with _allocating_on(batch.stream):
         refs = torch.empty(pool, dtype=torch.int32, device=batch.workspace.device)
     ric.ric_block_refs(batch.h, refs.data_ptr(), group)
@@ -470,6 +491,6 @@ def block_refs(batch: "Batch", group: int = 0) -> torch.Tensor:
 def fork_request(batch: "Batch", parent_id: int, child_id: int, num_tokens: int, num_computed: int, new_blocks,
                  kc: List[torch.Tensor], vc: List[torch.Tensor], sampling=None) -> int:
     """A new request over the parent's history, sharing its full pages (ric_fork_request)."""
-    k, v, n = _pages(kc, vc, batch.workspace.get_device())
+    k, v, n = _pages(batch, kc, vc, 0, new_blocks[:1])
     return ric.ric_fork_request(batch.h, parent_id, child_id, num_tokens, num_computed, new_blocks, k, v,
                                 n // batch.cfg.block_size, sampling)

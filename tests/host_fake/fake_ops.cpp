@@ -47,6 +47,7 @@ hipError_t launch_fork(const ForkParams& p, bool rows, hipStream_t) {
 size_t attention_workspace(const AttnParams&) { return 0; }
 hipError_t launch_attention(const AttnParams&, void*, hipStream_t) { return hipSuccess; }
 size_t logprobs_workspace(int32_t, int32_t, int32_t) { return 0; }
+size_t logprobs_workspace_up_to(int32_t, int32_t, int32_t) { return 0; }
 hipError_t launch_logprobs(const LogprobParams&, void*, hipStream_t) { return hipSuccess; }
 
 }  // namespace ric

@@ -143,6 +143,23 @@ def test_pages_that_name_nothing_are_left_out(runner, dim):
     assert status.item() > 0
 
 
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("seq", [2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30])
+def test_a_length_far_past_the_table(runner, dim, seq):
+    """Only the table's keys are there; every query stands behind them all."""
+    for reqs in ([(1, 90), (1, 64)], [(1, 90), (150, 200)], [(40, 90), (1, 64)]):
+        inp = attention_inputs(reqs, heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16, seed=5)
+        width = inp["table"].shape[1]
+        inp["lens"] = [(n, width * 16) for n, _ in reqs]
+        want, tol = attention_reference(inp, scale=0.1, prefix=[width * 16] * 2)
+        inp["seq"].fill_(seq)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        check_attention(call(runner, inp, scale=0.1, status=status, max_seq=200), want, tol)
+        assert status.item() > 0
+        got = call(runner, inp, scale=0.1, window=30, status=status, max_seq=200)
+        assert (got == 0).all()
+
+
 def test_a_request_longer_than_declared_is_left_alone(runner):
     reqs = [(1, 30), (50, 60), (1, 40)]
     for heads, dim in ((4, 128), (4, 24)):

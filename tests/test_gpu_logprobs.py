@@ -152,6 +152,16 @@ def test_device_count_leaves_the_rest(runner, vocab):
             assert (z[n:] == -5).all()
 
 
+def test_outputs_of_many_rows_take_fewer(runner):
+    """Few rows are cut into pieces that many rows are not."""
+    x, t = draw(1024, 16500, torch.bfloat16, seed=3)
+    o = runner.alloc_logprobs(1024, 16500, 5)
+    want = logprob_reference(x, t, 5)
+    for n in (1024, 1000, 600, 511, 2, 1):
+        runner.token_logprobs(x[:n], t[:n], 5, o)
+        compare(o, tuple(z[:n] for z in want), n, 16500, f"{n} rows")
+
+
 @pytest.mark.parametrize("rows,vocab", [(3, 50257), (400, 2000)])
 def test_stream_graph_and_equal_bits(runner, rows, vocab):
     sets = [draw(rows, vocab, torch.bfloat16, seed=s) for s in range(3)]

@@ -95,6 +95,25 @@ def test_more_pages_than_one_launch_holds(rt):
     b.close()
 
 
+def test_pages_past_the_caches_are_refused(rt):
+    ric, runner = rt
+    b, *_ = make(rt, groups=2, pool=400, reqs=3)
+    kc, vc = caches(2, 100, 16, 16, 5)
+    for src, dst in (([1, 100], [2, 3]), ([1, 2], [3, 399])):
+        for call in (runner.copy_blocks, runner.move_blocks):
+            with pytest.raises(ValueError):
+                call(b, src, dst, kc, vc)
+    with pytest.raises(ValueError):
+        runner.copy_blocks(b, [1], [2], kc, vc[:1])
+    for group in (-1, 2):
+        with pytest.raises(ValueError):
+            runner.copy_blocks(b, [1], [2], kc, vc, group)
+        with pytest.raises(ValueError):
+            runner.block_refs(b, group)
+    runner.copy_blocks(b, [1], [99], kc, vc)
+    b.close()
+
+
 @pytest.mark.parametrize("group", [0, 1])
 def test_compaction_moves_pages_and_tables(rt, group):
     """refs -> plan -> move: the used pages become the lowest ones, every live

@@ -93,6 +93,40 @@ def test_logprobs_refusals(ric):
             assert code(ric, ric.ric_token_logprobs, **{**ok, "max_rows": 1, "vocab": 150000, **ws}) == ric.RIC_EINVAL
 
 
+def test_logprobs_sizes(ric):
+    """A workspace of a row count is enough for every smaller one."""
+    for vocab, k in ((8192, 5), (16384, 0), (60001, 3), (151936, 64), (1 << 30, 64)):
+        last = 0
+        for rows in (1, 2, 3, 31, 32, 33, 100, 511, 512, 513, 1000, 1023, 1024, 5000, 1 << 22):
+            need = ric.ric_token_logprobs_workspace_bytes(rows, vocab, k)
+            pieces = max(1, min(-(-1024 // rows), vocab // 8192, 32))
+            assert need >= max(last, 0 if pieces == 1 else rows * pieces * (16 + 8 * k))
+            last = need
+        assert last < 4 << 20
+    assert ric.ric_token_logprobs_workspace_bytes(1, (1 << 30) + 1, 5) == 0
+    assert code(ric, ric.ric_token_logprobs, logits=4096, dtype=ric.RIC_BF16, targets=0, max_rows=1,
+                vocab=(1 << 30) + 1, top_k=0, logprob=0, rank=0, entropy=0, top_ids=0, top_logprobs=0) == ric.RIC_EINVAL
+
+
+def test_tensors_that_overlap_themselves_are_refused():
+    """Expanded and overlapping rows have no stride the calls could take."""
+    import torch
+    from ragged_input_compilation_amd import runner
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    q, cache, table, qsl, seq = bf(2, 4, 64), bf(5, 16, 2, 64), i32(2, 3), i32(3), i32(2)
+    call = lambda q=q, table=table, out=None: runner.paged_attention(q, cache, cache, table, qsl, seq, 1, 40,
+                                                                     bf(2, 4, 64) if out is None else out)
+    for kw in (dict(q=bf(1, 4, 64).expand(2, 4, 64)), dict(out=bf(1, 4, 64).expand(2, 4, 64)),
+               dict(q=bf(600).as_strided((2, 4, 64), (128, 64, 1))), dict(table=i32(1, 3).expand(2, 3)),
+               dict(table=i32(9).as_strided((2, 3), (2, 1)))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for logits in (bf(1, 100).expand(4, 100), bf(400).as_strided((4, 100), (50, 1))):
+        with pytest.raises(ValueError):
+            runner.token_logprobs(logits, None, 0)
+
+
 def test_compact_plan(ric):
     rng = np.random.default_rng(0)
     for _ in range(300):
