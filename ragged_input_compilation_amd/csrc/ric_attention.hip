@@ -30,12 +30,22 @@ __device__ __forceinline__ uint16_t to_bits16(float x, bool bf16) {
     return __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
-// 2^(x log2 e) and tanh of float32: errors of a few units in the last place,
-// far below the 8 or 11 bits of the outputs.
-__device__ __forceinline__ float tanh_f32(float x) {
-    const float e = __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
-    return 1.f - 2.f * __builtin_amdgcn_rcpf(e + 1.f);
+// tanh(x) from y = 2 x log2 e: an error of a few 2^-24, far below the 8 or 11 bits
+// of the outputs.
+__device__ __forceinline__ float tanh_of(float y) {
+    return 1.f - 2.f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y) + 1.f);
 }
+
+// Factors of a call that hold for every score: products q.k come to units of log2
+// by `log2`; under a cap by cap * tanh_of(q.k * arg).  Kept finite, so that a
+// product of 0 stays 0 under the largest scales.
+struct Factors {
+    float log2, arg, cap;
+    __device__ static float finite(float x) { return fminf(fmaxf(x, -3.4028235e38f), 3.4028235e38f); }
+    __device__ explicit Factors(const AttnParams& p)
+        : log2(finite(p.scale * kLog2e)), arg(p.cap > 0.f ? finite(p.scale / p.cap * (2.f * kLog2e)) : 0.f),
+          cap(finite(p.cap * kLog2e)) {}
+};
 
 __device__ __forceinline__ void raise(int32_t* status) {
     if (status != nullptr) atomicAdd(status, 1);
@@ -217,6 +227,7 @@ __device__ __forceinline__ void rows_group(const AttnParams& p, const Partial& p
     const uint8_t* kbase = p.kc + (int64_t)kvh * dim * 2 + g * 16;
     const uint8_t* vbase = p.vc + (int64_t)kvh * dim * 2 + g * 16;
     uint8_t* my = lds + w * WAVE_LDS;
+    const Factors by(p);
 
     // the query rows (token r / G, head r % G), and their positions and slopes
     u32x4 q[NB][DC];
@@ -343,18 +354,17 @@ __device__ __forceinline__ void rows_group(const AttnParams& p, const Partial& p
         for (int b = 0; b < NB; ++b) {
             float x[8];
             sees[b] = ~0u;
+            if (p.cap > 0.f) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+                for (int e = 0; e < 8; ++e) x[e] = by.cap * tanh_of(sc[b][e >> 2][e & 3] * by.arg);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = sc[b][s][e] * p.scale;
-                    if (p.cap > 0.f) v = p.cap * tanh_f32(v / p.cap);
-                    x[4 * s + e] = v * kLog2e;
-                }
+                for (int e = 0; e < 8; ++e) x[e] = sc[b][e >> 2][e & 3] * by.log2;
+            }
             if (p.slopes != nullptr) {
+                const float d = (float)(pos[b] - (j0 + 4 * g));      // exact below 2^24, as all its steps
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[e] -= slope[b] * fabsf((float)(pos[b] - (j0 + 16 * (e >> 2) + 4 * g + (e & 3))));
+                for (int e = 0; e < 8; ++e) x[e] -= slope[b] * fabsf(d - (float)(16 * (e >> 2) + (e & 3)));
             }
             if (!clear) {
                 // keys [lo, hi) of the tile, less those without a page; selected
@@ -535,7 +545,8 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const int32_t* ta
     float* qs = reinterpret_cast<float*>(scratch);
     float* ps = qs + 256;
     int64_t* at = reinterpret_cast<int64_t*>(ps + 64);
-    const float slope = p.slopes != nullptr ? p.slopes[head] : 0.f;
+    const float slope = p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.f;
+    const Factors by(p);
     const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q + (int64_t)tok * p.q_stride) + (int64_t)head * p.dim;
     for (int d = lane; d < p.dim; d += 64) qs[d] = from_bits16(q[d], p.bf16);
     const int64_t row_bytes = (int64_t)p.kv_heads * p.dim * 2;
@@ -556,9 +567,8 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const int32_t* ta
                     dot = fmaf(from_bits16(k[e] >> 16, p.bf16), qs[d + 2 * e + 1], dot);
                 }
             }
-            s = dot * p.scale;
-            if (p.cap > 0.f) s = p.cap * tanh_f32(s / p.cap);
-            s = (s - slope * fabsf((float)(pos - j))) * kLog2e;
+            s = p.cap > 0.f ? by.cap * tanh_of(dot * by.arg) : dot * by.log2;
+            s -= slope * fabsf((float)(pos - j));
         }
         float top = s;
         for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
@@ -723,7 +733,8 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
         }
     }
     // scores in units of log2: x = c s (FEAT: x computed in full, c = 1)
-    const float c = FEAT ? 1.f : fabsf(p.scale) * kLog2e;
+    const Factors by(p);
+    const float c = FEAT ? 1.f : fabsf(by.log2);
     const float slope = FEAT && p.slopes != nullptr && in ? p.slopes[head] * kLog2e : 0.f;
 
     // the keys that the tile's rows can see
@@ -836,17 +847,25 @@ __device__ __forceinline__ void chunk_group(const AttnParams& p, const Cut& cut,
             }
         }
         if constexpr (FEAT) {
+            if (p.cap > 0.f) {
 #pragma unroll
-            for (int b = 0; b < KB; ++b)
+                for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float v = s[b][e] * p.scale;
-                    if (p.cap > 0.f) v = p.cap * tanh_f32(v / p.cap);
-                    v *= kLog2e;
-                    if (p.slopes != nullptr)
-                        v -= slope * fabsf((float)(pos - (j0 + b * 32 + 8 * (e >> 2) + 4 * h32 + (e & 3))));
-                    s[b][e] = v;
-                }
+                    for (int e = 0; e < 16; ++e) s[b][e] = by.cap * tanh_of(s[b][e] * by.arg);
+            } else {
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[b][e] *= by.log2;
+            }
+            if (p.slopes != nullptr) {
+                const float d = (float)(pos - (j0 + 4 * h32));       // exact below 2^24, as all its steps
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s[b][e] -= slope * fabsf(d - (float)(b * 32 + 8 * (e >> 2) + (e & 3)));
+            }
         }
         const bool clear = !gaps && j0 + KT <= all_see_to && (p.window == 0 || j0 > p_wave_last - p.window);
         if (!clear) {

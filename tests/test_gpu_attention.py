@@ -144,6 +144,20 @@ def test_pages_that_name_nothing_are_left_out(runner, dim):
 
 
 @pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=1e-38), dict(softcap=3e38), dict(slopes=[0.5, 0.0, 1.0, 0.25])],
+                         ids=["plain", "small-cap", "large-cap", "bias"])
+def test_largest_scales_of_no_score(runner, dim, kw):
+    """Queries of zeros under factors that pass float32's range when multiplied."""
+    inp = attention_inputs([(1, 90), (80, 130), (3, 40)], heads=4, kv_heads=2, dim=dim, block=16, dtype=torch.bfloat16,
+                           seed=6, scale_q=0.0)
+    for scale in (3.3e38, -3.3e38):
+        both(runner, inp, scale=scale, **kw)
+        inp2 = {**inp, "q": inp["q"][:1], "lens": inp["lens"][:1], "qsl": inp["qsl"][:2], "seq": inp["seq"][:1],
+                "table": inp["table"][:1]}
+        both(runner, inp2, scale=scale, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 40])
 @pytest.mark.parametrize("seq", [2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30])
 def test_a_length_far_past_the_table(runner, dim, seq):
     """Only the table's keys are there; every query stands behind them all."""
